@@ -1,0 +1,510 @@
+// Per-head norm + rotation, and the quantised paged cache written and read.
+//
+// One kernel (head_rows_kernel) serves the norm + rotation, the append and
+// both in one pass; they differ in which rows of heads it is given and in
+// where a finished row goes.  All of it is bound by memory traffic (or, for a
+// few tokens, by latency): D/8 lanes hold a head's row, 8 elements (one
+// 16-byte load) each, so the mean square is a butterfly over those lanes, a
+// rotation partner is one shuffle away and a scale block of 32 is 4 lanes.
+#include <cmath>
+
+#include "moe_kv.cuh"
+
+namespace moe {
+
+moe_status_t kv_args(const moe_kv_cache_t* c, const moe_kv_batch_t* b, KvArgs* out) {
+  if (!c || !b || !c->data || !c->status || !b->block_table || !b->seq_lens || !b->cu_tokens) return MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)c->data & 15) || ((uintptr_t)c->status & 3) || ((uintptr_t)b->block_table & 3) ||
+      ((uintptr_t)b->seq_lens & 3) || ((uintptr_t)b->cu_tokens & 3))
+    return MOE_ERR_INVALID_ARG;
+  const size_t page = moe_kv_page_bytes(c->page_size, c->n_kv_heads, c->head_dim, c->bits);
+  if (!page || c->n_pages < 1 || c->data_bytes / page < (size_t)c->n_pages) return MOE_ERR_INVALID_ARG;
+  if (b->n_seqs < 1 || b->n_seqs > 65536 || b->max_pages < 1 || b->table_stride < b->max_pages || b->n_tokens < 0)
+    return MOE_ERR_INVALID_ARG;
+  if ((int64_t)b->max_pages * c->page_size > INT32_MAX) return MOE_ERR_INVALID_ARG;
+  if (b->n_tokens > 0 && (b->max_tokens < 1 || b->max_tokens > b->n_tokens)) return MOE_ERR_INVALID_ARG;
+  int shift = -1;
+  for (int s = 5; s <= 12; ++s)
+    if (c->page_size == 1 << s) shift = s;
+  *out = KvArgs{(uint8_t*)c->data, c->status,     b->block_table, b->seq_lens,     b->cu_tokens, c->n_pages,
+                c->page_size,      shift,         c->n_kv_heads,  b->table_stride, b->max_pages, b->n_seqs,
+                b->n_tokens,       b->max_tokens, page,           page / c->n_kv_heads};
+  return MOE_OK;
+}
+
+bool heads_ok(const moe_heads_t* h, int dim) {
+  return h && h->data && !((uintptr_t)h->data & 15) && h->token_stride >= 0 && h->head_stride >= 0 &&
+         h->token_stride % 8 == 0 && h->head_stride % 8 == 0 && (h->token_stride == 0 || h->token_stride >= dim) &&
+         (h->head_stride == 0 || h->head_stride >= dim);
+}
+
+bool out_heads_ok(const moe_heads_t* h, int n_heads, int n_tokens, int dim) {
+  return heads_ok(h, dim) && (n_heads <= 1 || h->head_stride) && (n_tokens <= 1 || h->token_stride);
+}
+
+moe_status_t device_sms(int* sms) {
+  constexpr int kMaxDevices = 64;
+  static int known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
+  int n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED);
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return MOE_ERR_CUDA;
+    __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
+  }
+  *sms = n;
+  return MOE_OK;
+}
+
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowsPerUnit = 4;  // heads of one token that a group of lanes takes when there are many rows
+
+struct HeadSrc {
+  const uint16_t* p;
+  int64_t ts, hs;
+};
+struct HeadDst {
+  uint16_t* p;
+  int64_t ts, hs;
+};
+
+struct RowArgs {
+  HeadSrc q, k, v;
+  HeadDst qo, ko;
+  const uint16_t *wq, *wk;
+  const float* table;
+  const int32_t* positions;
+  int n_positions, rot, inter;
+  float eps, woff;
+  int n_tokens, nq, nk, dim, slots;  // slots: units of a token
+};
+
+// x [8] of a scale block's 4 lanes -> the block's fp16 scale, and this lane's
+// 8 integers packed (8 bytes, or 4 bytes in x of the result).
+template <int BITS>
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint16_t& scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);  // a NaN is above infinity, infinity above every number
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  constexpr float top = BITS == 8 ? 127.f : 7.f, low = BITS == 8 ? -127.f : -8.f;
+  constexpr int bias = BITS == 8 ? 128 : 8;
+  scale = __half_as_ushort(__float2half_rn(__uint_as_float(m) / top));
+  if (m > 0x477E0000u) scale = 0x7FFFu;  // above 65024 (NaN and infinity among them): the block reads back as NaN
+  const float d = __half2float(__ushort_as_half(scale));
+  uint32_t u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float r = d > 0.f ? fminf(fmaxf(rintf(x[j] / d), low), top) : 0.f;
+    u[j] = (uint32_t)((int)r + bias);
+  }
+  if (BITS == 8)
+    return make_uint2(u[0] | u[1] << 8 | u[2] << 16 | u[3] << 24, u[4] | u[5] << 8 | u[6] << 16 | u[7] << 24);
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w |= u[j] << (4 * j);
+  return make_uint2(w, 0u);
+}
+
+// LPR lanes a row.  NORM: q and k rows are normalised and rotated.  BITS > 0:
+// k and v rows go to the cache (else k goes to ko and there is no v).
+template <int LPR, bool BF16, bool NORM, int BITS>
+__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowArgs r, const KvArgs kv) {
+  constexpr bool STORE = BITS > 0;
+  const int lane = threadIdx.x % LPR;
+  const uint32_t unit = blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR;
+  const int t = (int)(unit / (uint32_t)r.slots), s = (int)(unit % (uint32_t)r.slots);
+  const int H = r.nq + r.nk + (STORE ? r.nk : 0);
+  bool live = t < r.n_tokens;
+  const bool in = lane * 8 < r.dim;
+  int pos = 0;
+  uint8_t* tile = nullptr;
+  if (STORE && live) {
+    const int b = kv_seq_of(kv, t);
+    live = b >= 0;
+    if (live) {
+      const int c0 = __ldg(kv.cu + b), n = __ldg(kv.cu + b + 1) - c0, len = __ldg(kv.lens + b);
+      pos = len - n + (t - c0);
+      if (pos >= 0) tile = kv_tile_of(kv, b, pos, kv_tile_bytes(LPR * 8, BITS));
+      if (lane == 0 && s == 0) {
+        const int bad = (n > len || n > kv.max_tokens ? MOE_KV_BAD_BATCH : 0) | (pos >= 0 && !tile ? MOE_KV_BAD_PAGE : 0);
+        if (bad) kv_flag(kv, bad);
+      }
+    }
+  }
+  const int row = pos & (kKvTile - 1);
+  int angle = pos;
+  if (NORM && live && r.positions) angle = __ldg(r.positions + t);
+  if (NORM && angle < 0) live = false;  // padding
+
+  uint4 x[kRowsPerUnit];
+#pragma unroll
+  for (int i = 0; i < kRowsPerUnit; ++i) {
+    const int h = s + i * r.slots;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (live && in && h < H) {
+      const HeadSrc& src = h < r.nq ? r.q : h < r.nq + r.nk ? r.k : r.v;
+      const int hh = h < r.nq ? h : h < r.nq + r.nk ? h - r.nq : h - r.nq - r.nk;
+      x[i] = *reinterpret_cast<const uint4*>(src.p + (int64_t)t * src.ts + hh * src.hs + lane * 8);
+    }
+  }
+  // cos and sin of this lane's 8 elements (a pair shares one)
+  float cs[8], sn[8];
+  int partner = lane;
+  float sign = 0.f, nan_pos = 0.f;
+  const int half8 = r.rot / 16;  // lanes of the rotated part's first half
+  if (NORM && r.rot > 0 && live) {
+    if (angle >= r.n_positions) {
+      nan_pos = __uint_as_float(0x7FFFFFFFu);
+    } else if (lane < 2 * half8) {
+      const float* tab = r.table + (int64_t)angle * r.rot;
+      if (r.inter) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(tab + lane * 8));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(tab + lane * 8) + 1);
+        cs[0] = a.x, sn[0] = a.y, cs[1] = a.z, sn[1] = a.w, cs[2] = b.x, sn[2] = b.y, cs[3] = b.z, sn[3] = b.w;
+      } else {
+        const bool first = lane < half8;
+        const float4* p = reinterpret_cast<const float4*>(tab + (first ? lane : lane - half8) * 16);
+        sign = first ? -1.f : 1.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 a = __ldg(p + j);
+          cs[2 * j] = a.x, sn[2 * j] = sign * a.y, cs[2 * j + 1] = a.z, sn[2 * j + 1] = sign * a.w;
+        }
+      }
+    }
+  }
+  if (NORM && lane < 2 * half8) partner = lane < half8 ? lane + half8 : lane - half8;
+#pragma unroll
+  for (int i = 0; i < kRowsPerUnit; ++i) {
+    const int h = s + i * r.slots;
+    if (i > 0 && i * r.slots >= H) break;  // uniform: no unit has an i-th row
+    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    if (NORM) {
+      float f[8], ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unpack2<BF16>(w[j], f[2 * j], f[2 * j + 1]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = rsqrtf(ss / (float)r.dim + r.eps) + nan_pos;
+      const uint16_t* wt = h < r.nq ? r.wq : r.wk;
+      uint4 wv = make_uint4(0, 0, 0, 0);
+      const bool weighted = wt != nullptr && in && h < r.nq + r.nk;
+      if (weighted) wv = __ldg(reinterpret_cast<const uint4*>(wt + lane * 8));
+      const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a, b;
+        unpack2<BF16>(ww[j], a, b);
+        f[2 * j] *= inv * (weighted ? a + r.woff : 1.f);
+        f[2 * j + 1] *= inv * (weighted ? b + r.woff : 1.f);
+      }
+      if (r.rot > 0) {
+        if (r.inter) {
+          if (lane < 2 * half8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a = f[2 * j], b = f[2 * j + 1];
+              f[2 * j] = a * cs[j] - b * sn[j];
+              f[2 * j + 1] = b * cs[j] + a * sn[j];
+            }
+          }
+        } else {
+          float g[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], partner, LPR);
+          if (sign != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * cs[j] + g[j] * sn[j];
+          }
+        }
+      }
+      if (!STORE || h < r.nq + r.nk) {  // a v row passes through
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack2<BF16>(f[2 * j], f[2 * j + 1]);
+      }
+    }
+    if (!STORE || h < r.nq) {
+      if (live && in && h < H) {
+        const HeadDst& dst = h < r.nq ? r.qo : r.ko;
+        const int hh = h < r.nq ? h : h - r.nq;
+        *reinterpret_cast<uint4*>(dst.p + (int64_t)t * dst.ts + hh * dst.hs + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    if (STORE) {
+      constexpr int B = STORE ? BITS : 8, R = kv_row_bytes(LPR * 8, B);
+      float f[8];
+      uint16_t scale;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unpack2<BF16>(w[j], f[2 * j], f[2 * j + 1]);
+      const uint2 u = quantise8<B>(f, scale);  // every lane: shuffles
+      if (live && tile && h >= r.nq && h < H) {
+        const bool is_v = h >= r.nq + r.nk;
+        uint8_t* base = tile + (size_t)(h - r.nq - (is_v ? r.nk : 0)) * kv.head_bytes + (is_v ? kv_half_bytes(LPR * 8, B) : 0);
+        const int turn = kv_turn(row) & (R / 16 - 1);
+        if (B == 8)
+          *reinterpret_cast<uint2*>(base + row * R + (((lane >> 1) ^ turn) << 4) + (lane & 1) * 8) = u;
+        else
+          *reinterpret_cast<uint32_t*>(base + row * R + (((lane >> 2) ^ turn) << 4) + (lane & 3) * 4) = u.x;
+        if ((lane & 3) == 0) reinterpret_cast<uint16_t*>(base + kKvTile * R)[(lane >> 2) * kKvTile + row] = scale;
+      }
+    }
+  }
+}
+
+// Neighbouring groups of lanes take neighbouring tokens of the same heads, so
+// that a tile's 2-byte scales (32 tokens side by side) come from the same
+// sectors; a unit reads kReadHeads heads' K and V with all loads in flight.
+constexpr int kReadHeads = 2;
+
+template <int LPR, bool BF16, int BITS>
+__global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const KvArgs kv, const HeadDst ko, const HeadDst vo, int slots) {
+  constexpr int D = LPR * 8, R = kv_row_bytes(D, BITS), HB = kv_half_bytes(D, BITS);
+  const int lane = threadIdx.x % LPR;
+  const int s = blockIdx.y, t = (int)(blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR);
+  if (t >= kv.n_tokens) return;
+  const int b = kv_seq_of(kv, t);
+  if (b < 0) return;
+  const int c0 = __ldg(kv.cu + b), n = __ldg(kv.cu + b + 1) - c0, len = __ldg(kv.lens + b);
+  const int pos = len - n + (t - c0);
+  const uint8_t* tile = pos >= 0 ? kv_tile_of(kv, b, pos, kv_tile_bytes(D, BITS)) : nullptr;
+  if (lane == 0 && s == 0) {
+    const int bad = (n > len || n > kv.max_tokens ? MOE_KV_BAD_BATCH : 0) | (pos >= 0 && !tile ? MOE_KV_BAD_PAGE : 0);
+    if (bad) kv_flag(kv, bad);
+  }
+  const int row = pos & (kKvTile - 1), turn = kv_turn(row) & (R / 16 - 1);
+  const int at = BITS == 8 ? row * R + (((lane >> 1) ^ turn) << 4) + (lane & 1) * 8
+                           : row * R + (((lane >> 2) ^ turn) << 4) + (lane & 3) * 4;
+  uint2 u[2 * kReadHeads];
+  uint16_t sc[2 * kReadHeads];
+#pragma unroll
+  for (int i = 0; i < 2 * kReadHeads; ++i) {
+    const int h = s + (i >> 1) * slots;
+    u[i] = make_uint2(0, 0);
+    sc[i] = 0x7FFFu;
+    if (tile && h < kv.heads) {
+      const uint8_t* base = tile + (size_t)h * kv.head_bytes + (i & 1) * HB;
+      if (BITS == 8)
+        u[i] = *reinterpret_cast<const uint2*>(base + at);
+      else
+        u[i].x = *reinterpret_cast<const uint32_t*>(base + at);
+      sc[i] = reinterpret_cast<const uint16_t*>(base + kKvTile * R)[(lane >> 2) * kKvTile + row];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * kReadHeads; ++i) {
+    const int h = s + (i >> 1) * slots;
+    if (h >= kv.heads) continue;
+    const float d = __half2float(__ushort_as_half(sc[i]));
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int q = BITS == 8 ? (int)(((j < 4 ? u[i].x : u[i].y) >> (8 * (j & 3))) & 255u) - 128
+                              : (int)((u[i].x >> (4 * j)) & 15u) - 8;
+      f[j] = d * (float)q;
+    }
+    const HeadDst& o = (i & 1) ? vo : ko;
+    *reinterpret_cast<uint4*>(o.p + (int64_t)t * o.ts + h * o.hs + lane * 8) =
+        make_uint4(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]), pack2<BF16>(f[4], f[5]), pack2<BF16>(f[6], f[7]));
+  }
+}
+
+HeadSrc src_of(const moe_heads_t* h) {
+  return h ? HeadSrc{(const uint16_t*)h->data, h->token_stride, h->head_stride} : HeadSrc{nullptr, 0, 0};
+}
+HeadDst dst_of(const moe_heads_t* h) {
+  return h ? HeadDst{(uint16_t*)h->data, h->token_stride, h->head_stride} : HeadDst{nullptr, 0, 0};
+}
+
+template <int LPR, bool NORM, int BITS>
+moe_status_t launch_rows(RowArgs r, const KvArgs& kv, bool bf16, cudaStream_t st) {
+  const int H = r.nq + r.nk + (BITS ? r.nk : 0);
+  // One row a group while that fills the GPU at most once over, so that a
+  // small call's rows all run side by side; several rows of a token a group
+  // above that, which reuses the token's angles and page.
+  const int64_t rows = (int64_t)r.n_tokens * H;
+  r.slots = rows * LPR <= 152 * 2048 ? H : (H + kRowsPerUnit - 1) / kRowsPerUnit;
+  if ((int64_t)r.n_tokens * r.slots > INT32_MAX - kRowThreads) return MOE_ERR_INVALID_ARG;
+  const int64_t blocks = ((int64_t)r.n_tokens * r.slots * LPR + kRowThreads - 1) / kRowThreads;
+  if (bf16)
+    head_rows_kernel<LPR, true, NORM, BITS><<<(int)blocks, kRowThreads, 0, st>>>(r, kv);
+  else
+    head_rows_kernel<LPR, false, NORM, BITS><<<(int)blocks, kRowThreads, 0, st>>>(r, kv);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <bool NORM>
+moe_status_t launch_store(const RowArgs& r, const KvArgs& kv, int bits, bool bf16, cudaStream_t st) {
+  if (bits == 8) {
+    if (r.dim == 64) return launch_rows<8, NORM, 8>(r, kv, bf16, st);
+    if (r.dim == 128) return launch_rows<16, NORM, 8>(r, kv, bf16, st);
+    return launch_rows<32, NORM, 8>(r, kv, bf16, st);
+  }
+  if (r.dim == 64) return launch_rows<8, NORM, 4>(r, kv, bf16, st);
+  if (r.dim == 128) return launch_rows<16, NORM, 4>(r, kv, bf16, st);
+  return launch_rows<32, NORM, 4>(r, kv, bf16, st);
+}
+
+template <int LPR, int BITS>
+moe_status_t launch_read(const KvArgs& kv, const HeadDst& ko, const HeadDst& vo, bool bf16, cudaStream_t st) {
+  const int slots = (kv.heads + kReadHeads - 1) / kReadHeads;
+  const dim3 grid((unsigned)(((int64_t)kv.n_tokens * LPR + kRowThreads - 1) / kRowThreads), slots);
+  if (bf16)
+    kv_read_kernel<LPR, true, BITS><<<grid, kRowThreads, 0, st>>>(kv, ko, vo, slots);
+  else
+    kv_read_kernel<LPR, false, BITS><<<grid, kRowThreads, 0, st>>>(kv, ko, vo, slots);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Fills the norm + rotation part of `r`; the activations are checked by the caller.
+moe_status_t norm_args(const moe_norm_rope_t* d, int dim, const int32_t* positions, bool need_positions, RowArgs* r) {
+  if (!d || !(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->weight_offset)) return MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)d->q_weight & 15) || ((uintptr_t)d->k_weight & 15)) return MOE_ERR_INVALID_ARG;
+  if (d->rot_dim < 0 || d->rot_dim % 16 || d->rot_dim > dim) return MOE_ERR_INVALID_ARG;
+  if (d->rot_dim > 0 && (!d->table || ((uintptr_t)d->table & 15) || d->n_positions < 1)) return MOE_ERR_INVALID_ARG;
+  if (d->rot_dim > 0 && need_positions && !positions) return MOE_ERR_INVALID_ARG;
+  if ((uintptr_t)positions & 3) return MOE_ERR_INVALID_ARG;
+  r->wq = (const uint16_t*)d->q_weight;
+  r->wk = (const uint16_t*)d->k_weight;
+  r->table = d->table;
+  r->positions = positions;
+  r->n_positions = d->n_positions;
+  r->rot = d->rot_dim;
+  r->inter = d->interleaved != 0;
+  r->eps = d->eps;
+  r->woff = d->weight_offset;
+  return MOE_OK;
+}
+
+moe_status_t half_type(int32_t dtype) {
+  if (dtype == MOE_BF16 || dtype == MOE_FP16) return MOE_OK;
+  return dtype == MOE_FP32 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" MOE_API size_t moe_kv_page_bytes(int32_t page_size, int32_t n_kv_heads, int32_t head_dim, int32_t bits) {
+  if (page_size < 32 || page_size > 4096 || page_size % 32 || n_kv_heads < 1 || n_kv_heads > 1024) return 0;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || (bits != 8 && bits != 4)) return 0;
+  return (size_t)n_kv_heads * (page_size / 32) * moe::kv_tile_bytes(head_dim, bits);
+}
+
+extern "C" MOE_API moe_status_t moe_rope_table(int32_t n_positions, int32_t rot_dim, double base, float* table_host) {
+  if (!table_host || n_positions < 1 || rot_dim < 16 || rot_dim % 16 || !(base > 0.0) || !std::isfinite(base))
+    return MOE_ERR_INVALID_ARG;
+  const int half = rot_dim / 2;
+  for (int i = 0; i < half; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot_dim);
+    for (int64_t p = 0; p < n_positions; ++p) {
+      table_host[(p * half + i) * 2] = (float)std::cos((double)p * f);
+      table_host[(p * half + i) * 2 + 1] = (float)std::sin((double)p * f);
+    }
+  }
+  return MOE_OK;
+}
+
+extern "C" MOE_API moe_status_t moe_qk_norm_rope(const moe_norm_rope_t* desc, int32_t dtype, int32_t n_tokens,
+                                                 int32_t head_dim, int32_t n_q, const moe_heads_t* q,
+                                                 const moe_heads_t* q_out, int32_t n_kv, const moe_heads_t* k,
+                                                 const moe_heads_t* k_out, const int32_t* positions, void* cuda_stream) {
+  moe_status_t st = moe::half_type(dtype);
+  if (st != MOE_OK) return st;
+  if (n_tokens < 0 || head_dim < 8 || head_dim > 256 || head_dim % 8 || n_q < 0 || n_kv < 0 || n_q > 65536 || n_kv > 65536)
+    return MOE_ERR_INVALID_ARG;
+  moe::RowArgs r{};
+  st = moe::norm_args(desc, head_dim, positions, n_tokens > 0, &r);
+  if (st != MOE_OK) return st;
+  if (n_tokens == 0 || n_q + n_kv == 0) return MOE_OK;
+  if (n_q && (!moe::heads_ok(q, head_dim) || !moe::out_heads_ok(q_out, n_q, n_tokens, head_dim))) return MOE_ERR_INVALID_ARG;
+  if (n_kv && (!moe::heads_ok(k, head_dim) || !moe::out_heads_ok(k_out, n_kv, n_tokens, head_dim))) return MOE_ERR_INVALID_ARG;
+  r.q = moe::src_of(n_q ? q : nullptr);
+  r.qo = moe::dst_of(n_q ? q_out : nullptr);
+  r.k = moe::src_of(n_kv ? k : nullptr);
+  r.ko = moe::dst_of(n_kv ? k_out : nullptr);
+  r.n_tokens = n_tokens;
+  r.nq = n_q;
+  r.nk = n_kv;
+  r.dim = head_dim;
+  const cudaStream_t s = (cudaStream_t)cuda_stream;
+  const moe::KvArgs none{};
+  if (head_dim <= 64) return moe::launch_rows<8, true, 0>(r, none, dtype == MOE_BF16, s);
+  if (head_dim <= 128) return moe::launch_rows<16, true, 0>(r, none, dtype == MOE_BF16, s);
+  return moe::launch_rows<32, true, 0>(r, none, dtype == MOE_BF16, s);
+}
+
+extern "C" MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t dtype,
+                                              const moe_heads_t* k, const moe_heads_t* v, void* cuda_stream) {
+  moe_status_t st = moe::half_type(dtype);
+  if (st != MOE_OK) return st;
+  moe::KvArgs kv;
+  st = moe::kv_args(cache, batch, &kv);
+  if (st != MOE_OK) return st;
+  if (kv.n_tokens == 0) return MOE_OK;
+  if (!moe::heads_ok(k, cache->head_dim) || !moe::heads_ok(v, cache->head_dim)) return MOE_ERR_INVALID_ARG;
+  moe::RowArgs r{};
+  r.k = moe::src_of(k);
+  r.v = moe::src_of(v);
+  r.n_tokens = kv.n_tokens;
+  r.nk = kv.heads;
+  r.dim = cache->head_dim;
+  return moe::launch_store<false>(r, kv, cache->bits, dtype == MOE_BF16, (cudaStream_t)cuda_stream);
+}
+
+extern "C" MOE_API moe_status_t moe_kv_append_norm_rope(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch,
+                                                        const moe_norm_rope_t* desc, int32_t dtype, int32_t n_q,
+                                                        const moe_heads_t* q, const moe_heads_t* q_out,
+                                                        const moe_heads_t* k, const moe_heads_t* v,
+                                                        const int32_t* positions, void* cuda_stream) {
+  moe_status_t st = moe::half_type(dtype);
+  if (st != MOE_OK) return st;
+  moe::KvArgs kv;
+  st = moe::kv_args(cache, batch, &kv);
+  if (st != MOE_OK) return st;
+  const int dim = cache->head_dim;
+  moe::RowArgs r{};
+  st = moe::norm_args(desc, dim, positions, false, &r);
+  if (st != MOE_OK) return st;
+  if (n_q < 0 || n_q > 65536) return MOE_ERR_INVALID_ARG;
+  if (kv.n_tokens == 0) return MOE_OK;
+  if (n_q && (!moe::heads_ok(q, dim) || !moe::out_heads_ok(q_out, n_q, kv.n_tokens, dim))) return MOE_ERR_INVALID_ARG;
+  if (!moe::heads_ok(k, dim) || !moe::heads_ok(v, dim)) return MOE_ERR_INVALID_ARG;
+  r.q = moe::src_of(n_q ? q : nullptr);
+  r.qo = moe::dst_of(n_q ? q_out : nullptr);
+  r.k = moe::src_of(k);
+  r.v = moe::src_of(v);
+  r.n_tokens = kv.n_tokens;
+  r.nq = n_q;
+  r.nk = kv.heads;
+  r.dim = dim;
+  return moe::launch_store<true>(r, kv, cache->bits, dtype == MOE_BF16, (cudaStream_t)cuda_stream);
+}
+
+extern "C" MOE_API moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t dtype,
+                                            const moe_heads_t* k_out, const moe_heads_t* v_out, void* cuda_stream) {
+  moe_status_t st = moe::half_type(dtype);
+  if (st != MOE_OK) return st;
+  moe::KvArgs kv;
+  st = moe::kv_args(cache, batch, &kv);
+  if (st != MOE_OK) return st;
+  if (kv.n_tokens == 0) return MOE_OK;
+  const int dim = cache->head_dim;
+  if (!moe::out_heads_ok(k_out, kv.heads, kv.n_tokens, dim) || !moe::out_heads_ok(v_out, kv.heads, kv.n_tokens, dim))
+    return MOE_ERR_INVALID_ARG;
+  const moe::HeadDst ko = moe::dst_of(k_out), vo = moe::dst_of(v_out);
+  const cudaStream_t s = (cudaStream_t)cuda_stream;
+  const bool bf = dtype == MOE_BF16;
+  if (cache->bits == 8) {
+    if (dim == 64) return moe::launch_read<8, 8>(kv, ko, vo, bf, s);
+    if (dim == 128) return moe::launch_read<16, 8>(kv, ko, vo, bf, s);
+    return moe::launch_read<32, 8>(kv, ko, vo, bf, s);
+  }
+  if (dim == 64) return moe::launch_read<8, 4>(kv, ko, vo, bf, s);
+  if (dim == 128) return moe::launch_read<16, 4>(kv, ko, vo, bf, s);
+  return moe::launch_read<32, 4>(kv, ko, vo, bf, s);
+}

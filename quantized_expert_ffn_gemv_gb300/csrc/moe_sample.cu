@@ -1,0 +1,652 @@
+// Sampling: one thread-block cluster a row.  The row is read from memory once,
+// as fp32 into the cluster's shared memory, and everything else happens
+// there: the maximum, the cut that top-k and top-p make, the kept mass, and
+// the token.  With the row at hand the bound is the one read of the logits;
+// for a single row it is the chain of cluster barriers.
+//
+// Weights w = 2^-y, y = (max - z) log2(e) / T, are evaluated to about 2^-32
+// relative (float pairs for y, a 256-entry table and a cubic for the rest)
+// and held as integers in units of 2^-45: integer sums have no order, so any
+// split of the work gives the same bits, and the sums that top-p, min-p and
+// the draw compare are exact.
+//
+// The cut.  Kept elements are a prefix of the order (logit descending, index
+// ascending).  A histogram of y (1/16 octave a bin; counts, and masses as two
+// 16-bit halves relative to the bin's octave) finds the bin the cut falls
+// into.  If few elements share it, they are collected in the first CTA and
+// ranked exactly; otherwise the bin's range of logits is histogrammed again,
+// finer, until few are left or all have the same logit, whose cut is then an
+// index.
+#include <cooperative_groups.h>
+#include <cmath>
+
+#include "moe_kv.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kSThreads = 512, kSWarps = kSThreads / 32;
+constexpr int kBins = 1024, kPerOctave = 16;  // 64 octaves: beyond them a weight is 0 in units of 2^-45
+constexpr int kUnit = 45;                     // 2^18 weights of 2^45 fit 64 bits
+constexpr int kList = 768;                    // elements ranked exactly at most
+constexpr int kMaxVocab = 262144;
+constexpr int kMaxCluster = 8;
+
+struct Pow2Table {
+  float hi[256], lo[256];
+};
+// 2^(-i/256) as float pairs: the exponential's power series in binary64.
+constexpr Pow2Table make_pow2() {
+  Pow2Table t{};
+  for (int i = 0; i < 256; ++i) {
+    const double x = -0.69314718055994530942 * i / 256.0;
+    double term = 1.0, sum = 1.0;
+    for (int n = 1; n < 24; ++n) {
+      term *= x / n;
+      sum += term;
+    }
+    t.hi[i] = (float)sum;
+    t.lo[i] = (float)(sum - (double)t.hi[i]);
+  }
+  return t;
+}
+__device__ const Pow2Table g_pow2 = make_pow2();
+
+struct SampleArgs {
+  const void* logits;
+  int64_t row_stride;
+  int rows, vocab, slice;
+  const float *u, *temperature, *top_p, *min_p;
+  const int32_t* top_k;
+  int32_t* tokens;
+  float* probs;
+};
+
+// log2(e) / T as a float pair.
+struct Rate {
+  float h, l;
+};
+__device__ __forceinline__ Rate rate_of(float T) {
+  const float lh = 1.44269502162933349609f, ll = 1.925963033500e-08f;  // log2(e)
+  Rate r;
+  r.h = lh / T;
+  r.l = (fmaf(-r.h, T, lh) + ll) / T;
+  return r;
+}
+
+// y of a logit z <= m rounded to fp32, which orders logits weakly; infinity for -infinity.
+__device__ __forceinline__ float y_of(float z, float m, const Rate& c) { return z == -INFINITY ? INFINITY : (m - z) * c.h; }
+__device__ __forceinline__ int bin_of(float y) { return y < 64.f ? (int)(y * kPerOctave) : kBins - 1; }
+
+// w relative to 2^-oct in units of 2^-32 (at most 2^32); 0 and oct 64 beyond 64 octaves.
+__device__ __forceinline__ uint64_t weight32(float z, float m, const Rate& c, const float2* tab, int& oct) {
+  const float yh = y_of(z, m, c);
+  if (!(yh < 64.f)) {
+    oct = 64;
+    return 0;
+  }
+  const float x = m - z, bb = x - m;
+  const float xl = (m - (x - bb)) + (-z - bb);  // m - z = x + xl
+  const float yl = fmaf(x, c.h, -yh) + fmaf(x, c.l, xl * c.h);
+  const float k = rintf(yh * 256.f);
+  const float r = (fmaf(k, -1.f / 256.f, yh) + yl) * 0.693147180559945f;
+  const float p = r * fmaf(r, fmaf(r, -1.f / 6.f, 0.5f), -1.f);  // e^-r - 1
+  const int ki = (int)k;
+  const float2 t = tab[ki & 255];
+  const float low = fmaf(t.x, p, t.y);
+  oct = ki >> 8;
+  return (uint64_t)((int64_t)(t.x * 4294967296.f) + (int64_t)rintf(low * 4294967296.f));
+}
+__device__ __forceinline__ uint64_t weight(float z, float m, const Rate& c, const float2* tab) {
+  int oct;
+  const uint64_t w = weight32(z, m, c, tab, oct);
+  return oct >= 64 ? 0 : ((w << (kUnit - 32)) + ((1ull << oct) >> 1)) >> oct;
+}
+
+// Order-preserving image of a logit (no NaN): larger logit, larger key; -0 equals 0.
+__device__ __forceinline__ uint32_t key_of(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
+// floor(x * f), or ceil(x * f) with up, for 0 <= f < 1, exactly.
+__device__ __forceinline__ uint64_t mul_frac(uint64_t x, float f, bool up) {
+  if (!(f > 0.f)) return 0;
+  const uint32_t b = __float_as_uint(f);
+  const int e = (int)(b >> 23);
+  const uint64_t mant = e ? (b & 0x7FFFFFu) | 0x800000u : (b & 0x7FFFFFu);
+  const int sh = 150 - (e ? e : 1);  // f = mant * 2^-sh, sh = 24 .. 149
+  const uint64_t lo = x * mant, hi = __umul64hi(x, mant);
+  uint64_t q, rest;
+  if (sh < 64) {
+    q = (hi << (64 - sh)) | (lo >> sh);
+    rest = lo << (64 - sh);
+  } else if (sh < 128) {
+    q = hi >> (sh - 64);
+    rest = lo | (sh == 64 ? 0 : hi << (128 - sh));
+  } else {
+    q = 0;
+    rest = lo | hi;
+  }
+  return q + (up && rest ? 1 : 0);
+}
+
+// The elements kept: those of a key above, or of the key itself up to an index.
+struct Cut {
+  uint32_t key, idx;
+};
+__device__ __forceinline__ bool kept(uint32_t key, uint32_t idx, const Cut& c) { return key > c.key || (key == c.key && idx <= c.idx); }
+
+struct Shared {
+  // this CTA's histogram; the list of the cut bin's elements takes its place later (first CTA)
+  union {
+    struct {
+      uint32_t count[kBins], hi[kBins], lo[kBins];
+    } h;
+    struct {
+      uint32_t key[kList], idx[kList];
+      uint64_t w[kList];
+    } list;
+  };
+  // the cluster's histogram (first CTA)
+  uint32_t mcount[kBins];
+  uint64_t mmass[kBins];
+  float2 pow2[256];
+  uint64_t wsum[kSWarps];
+  uint32_t wcnt[kSWarps];
+  float wmax[kSWarps];
+  // written by the CTA, read by the cluster
+  float cmax;
+  uint32_t cfirst, ccount;  // greedy: the maximum's lowest index; find_cut: lowest and highest key, or a count
+  uint64_t ctotal;
+  // written by the first CTA, read by the cluster
+  uint32_t list_n;
+  int cut_bin;
+  uint32_t cut_count, cut_need;
+  uint64_t cut_before;
+  Cut cut;
+  int found;
+};
+
+// Exclusive prefixes of a count and a mass over the block's threads.
+__device__ __forceinline__ void block_scan(Shared& s, uint32_t& c, uint64_t& m) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t ci = c;
+  uint64_t mi = m;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t cv = __shfl_up_sync(0xffffffffu, ci, o);
+    const uint64_t mv = __shfl_up_sync(0xffffffffu, mi, o);
+    if (lane >= o) ci += cv, mi += mv;
+  }
+  __syncthreads();
+  if (lane == 31) s.wcnt[warp] = ci, s.wsum[warp] = mi;
+  __syncthreads();
+  uint32_t cb = 0;
+  uint64_t mb = 0;
+  for (int w = 0; w < warp; ++w) cb += s.wcnt[w], mb += s.wsum[w];
+  c = cb + ci - c;
+  m = mb + mi - m;
+}
+
+// The slice of a row that a CTA holds.
+struct Slice {
+  const float* z;
+  int n;
+  uint32_t base;
+  float m;
+  Rate c;
+};
+
+// The cut among the elements that `limit` keeps (all, when not limited): at
+// the need-th of the order, or, by mass, at the first where the running mass
+// reaches the target.  The whole cluster calls it; the result is in the
+// first CTA's Shared::cut afterwards, until the caller's next cluster barrier.
+__device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, const Slice& v, const Cut limit, bool limited,
+                         bool by_mass, uint32_t need, uint64_t target) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
+  int level = 0, shift = 0, octave = 0, bin0 = 0;
+  uint32_t top_key = 0, low_key = 0;  // level > 0: the range of keys looked at
+  uint64_t before = 0;                // mass in front of the range
+  // is element i among those looked at, and in which bin
+  auto place = [&](int i, float z, uint32_t key) -> int {
+    if (limited && !kept(key, v.base + i, limit)) return -1;
+    const int b0 = bin_of(y_of(z, v.m, v.c));
+    if (level == 0) return b0;
+    return b0 == bin0 && key <= top_key && key >= low_key ? (int)((top_key - key) >> shift) : -1;
+  };
+  for (;;) {
+    for (int i = tid; i < kBins; i += kSThreads) s.h.count[i] = s.h.hi[i] = s.h.lo[i] = 0;
+    __syncthreads();
+    for (int i0 = 0; i0 < v.n; i0 += kSThreads) {
+      const int i = i0 + tid;
+      int bin = -1;
+      uint64_t w = 0;
+      if (i < v.n) {
+        const float z = v.z[i];
+        bin = place(i, z, key_of(z));
+        if (bin >= 0 && by_mass) {
+          int oct;
+          w = weight32(z, v.m, v.c, s.pow2, oct);
+          // the bin's octave is at most one below the weight's
+          w >>= min(oct - (level == 0 ? bin / kPerOctave : octave), 63);
+        }
+      }
+      // the far end collects most elements when the temperature is low: one atomic a warp
+      const unsigned far = __ballot_sync(0xffffffffu, bin == kBins - 1);
+      if (bin >= 0 && bin < kBins - 1) atomicAdd(&s.h.count[bin], 1u);
+      if (far && lane == __ffs(far) - 1) atomicAdd(&s.h.count[kBins - 1], (uint32_t)__popc(far));
+      if (w) {
+        atomicAdd(&s.h.hi[bin], (uint32_t)(w >> 16));
+        atomicAdd(&s.h.lo[bin], (uint32_t)(w & 0xFFFFu));
+      }
+    }
+    cluster.sync();
+    // every CTA adds up its share of the bins over the cluster, for the first one
+    for (int i = rank * (kBins / C) + tid; i < (rank + 1) * (kBins / C); i += kSThreads) {
+      uint32_t cnt = 0;
+      uint64_t mass = 0;
+      for (int r = 0; r < C; ++r) {
+        const Shared* o = cluster.map_shared_rank(&s, r);
+        cnt += o->h.count[i];
+        mass += ((uint64_t)o->h.hi[i] << 16) + o->h.lo[i];
+      }
+      s0->mcount[i] = cnt;
+      s0->mmass[i] = (mass << (kUnit - 32)) >> (level == 0 ? i / kPerOctave : octave);
+    }
+    cluster.sync();
+    if (rank == 0) {
+      constexpr int kPer = kBins / kSThreads;
+      uint32_t cnt[kPer], cb = 0;
+      uint64_t mass[kPer], mb = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        cb += cnt[j] = s.mcount[tid * kPer + j];
+        mb += mass[j] = s.mmass[tid * kPer + j];
+      }
+      if (tid == 0) s.cut_bin = -1, s.list_n = 0;
+      block_scan(s, cb, mb);
+      mb += before;
+      int last = -1;  // the thread's last bin that counts
+      uint64_t last_before = 0;
+      uint32_t last_count = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const bool here = by_mass ? mb < target && target <= mb + mass[j] : cb < need && need <= cb + cnt[j];
+        if (here) {
+          s.cut_bin = tid * kPer + j;
+          s.cut_count = cnt[j];
+          s.cut_need = need - cb;
+          s.cut_before = mb;
+        }
+        if (cnt[j] && (!by_mass || mass[j])) last = tid * kPer + j, last_before = mb, last_count = cnt[j];
+        cb += cnt[j];
+        mb += mass[j];
+      }
+      __syncthreads();
+      if (s.cut_bin < 0) {  // the bins' masses, each rounded down, end a little below the target: the last bin that counts
+        const int best = __reduce_max_sync(0xffffffffu, last);
+        if (lane == 0) s.wcnt[warp] = (uint32_t)(best + 1);
+        __syncthreads();
+        int all = 0;
+        for (int w = 0; w < kSWarps; ++w) all = max(all, (int)s.wcnt[w]);
+        if (last >= 0 && last == all - 1) {
+          s.cut_bin = last;
+          s.cut_count = last_count;
+          s.cut_need = last_count;
+          s.cut_before = last_before;
+        }
+      }
+    }
+    cluster.sync();
+    const int bin = s0->cut_bin;
+    const uint32_t count = s0->cut_count;
+    before = s0->cut_before;
+    if (!by_mass) need = s0->cut_need;
+    const bool one_key = level > 0 && shift == 0;
+    if (level == 0) {
+      bin0 = bin;
+      octave = bin / kPerOctave;
+    } else {
+      top_key -= (uint32_t)bin << shift;
+      const uint32_t span = shift ? (1u << shift) - 1u : 0u;
+      low_key = top_key - low_key > span ? top_key - span : low_key;
+    }
+    if (count <= kList) {
+      // collect the bin's elements in the first CTA, rank them all against all
+      for (int i = tid; i < v.n; i += kSThreads) {
+        const float z = v.z[i];
+        const uint32_t key = key_of(z);
+        const int b = place(i, z, key);
+        if (level == 0 ? b != bin0 : b < 0) continue;
+        const uint32_t at = atomicAdd(&s0->list_n, 1u);
+        if (at < kList) {
+          s0->list.key[at] = key;
+          s0->list.idx[at] = v.base + i;
+          s0->list.w[at] = weight(z, v.m, v.c, s.pow2);
+        }
+      }
+      cluster.sync();
+      if (rank == 0) {
+        const int n = (int)min(s.list_n, (uint32_t)kList);
+        if (tid == 0) s.found = 0;
+        __syncthreads();
+        for (int pass = 0; pass < 2; ++pass) {
+          for (int e = tid; e < n; e += kSThreads) {
+            const uint32_t k = s.list.key[e], x = s.list.idx[e];
+            uint32_t rank_e = 0;
+            uint64_t front = before;
+            for (int j = 0; j < n; ++j) {
+              const uint32_t kj = s.list.key[j], xj = s.list.idx[j];
+              const bool ahead = kj > k || (kj == k && xj < x);
+              rank_e += ahead;
+              front += ahead ? s.list.w[j] : 0;
+            }
+            // the need-th; or the one whose weight takes the mass to the target (the last, should rounding leave none)
+            bool last = by_mass ? front < target && (target <= front + s.list.w[e] || rank_e == (uint32_t)n - 1) : rank_e == need - 1;
+            if (pass == 1) last = rank_e == 0;  // what lies in front reached the target by rounding: the bin's first
+            if (last) {
+              s.cut = Cut{k, x};
+              s.found = 1;
+            }
+          }
+          __syncthreads();
+          if (s.found) break;
+        }
+      }
+      cluster.sync();
+      return;
+    }
+    if (one_key) {
+      // all `count` elements have the key top_key and one weight: the cut is the want-th of them in index order
+      const uint32_t k = top_key;
+      uint32_t want = need;
+      if (by_mass) {
+        const uint64_t w = weight(logit_of(k), v.m, v.c, s.pow2), more = target > before ? target - before : 1;
+        want = w ? (uint32_t)min((more + w - 1) / w, (uint64_t)count) : count;
+      }
+      const int seg = (v.n + kSWarps - 1) / kSWarps, lo = min(warp * seg, v.n), hi = min(lo + seg, v.n);
+      auto equal = [&](int i) { return i < hi && key_of(v.z[i]) == k && (!limited || kept(k, v.base + i, limit)); };
+      uint32_t mine = 0;
+      for (int i0 = lo; i0 < hi; i0 += 32) mine += __popc(__ballot_sync(0xffffffffu, equal(i0 + lane)));
+      if (lane == 0) s.wcnt[warp] = mine;
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t all = 0;
+        for (int x = 0; x < kSWarps; ++x) all += s.wcnt[x];
+        s.ccount = all;
+      }
+      cluster.sync();
+      uint32_t front = 0;
+      for (int r = 0; r < rank; ++r) front += cluster.map_shared_rank(&s, r)->ccount;
+      for (int x = 0; x < warp; ++x) front += s.wcnt[x];
+      if (front < want && want <= front + mine) {
+        for (int i0 = lo; i0 < hi; i0 += 32) {
+          const bool eq = equal(i0 + lane);
+          const unsigned b = __ballot_sync(0xffffffffu, eq);
+          if (eq && front + __popc(b & ((1u << lane) - 1u)) + 1 == want) s0->cut = Cut{k, v.base + i0 + lane};
+          front += __popc(b);
+        }
+      }
+      cluster.sync();
+      return;
+    }
+    // the bin again, finer: first the keys it spans
+    if (level == 0) {
+      uint32_t hi = 0, lo = 0xFFFFFFFFu;
+      for (int i = tid; i < v.n; i += kSThreads) {
+        const float z = v.z[i];
+        const uint32_t key = key_of(z);
+        if (place(i, z, key) == bin0) hi = max(hi, key), lo = min(lo, key);
+      }
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      if (tid == 0) s.cfirst = 0xFFFFFFFFu, s.ccount = 0;
+      __syncthreads();
+      if (lane == 0) {
+        atomicMax(&s.ccount, hi);
+        atomicMin(&s.cfirst, lo);
+      }
+      cluster.sync();
+      for (int r = 0; r < C; ++r) {
+        const Shared* o = cluster.map_shared_rank(&s, r);
+        hi = max(hi, o->ccount);
+        lo = min(lo, o->cfirst);
+      }
+      top_key = hi;
+      low_key = lo;
+    }
+    shift = 0;
+    while (((top_key - low_key) >> shift) >= (uint32_t)(kBins - 1)) ++shift;  // the far bin stays free
+    ++level;
+    cluster.sync();  // ccount, cfirst and the cut have been read
+  }
+}
+
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
+
+template <typename T>
+__global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  float* z = reinterpret_cast<float*>(smem + sizeof(Shared));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
+  const int row = blockIdx.x / C;
+  Shared* s0 = cluster.map_shared_rank(&s, 0);
+  const uint32_t base = (uint32_t)rank * a.slice;
+  const int n = max(0, min(a.slice, a.vocab - (int)base));
+  const T* src = reinterpret_cast<const T*>(a.logits) + (int64_t)row * a.row_stride + base;
+
+  // the one read: scalar up to a 16-byte boundary, 16 bytes a thread from there
+  constexpr int kVec = 16 / sizeof(T);
+  float top = -INFINITY;
+  auto put = [&](int i, float v) {
+    v = v != v ? -INFINITY : v;  // a NaN ranks below every number and weighs nothing, like -infinity
+    z[i] = v;
+    top = fmaxf(top, v);
+  };
+  const int head = min(n, (int)(((16 - ((uintptr_t)src & 15)) & 15) / sizeof(T)));
+  const int vecs = (n - head) / kVec;
+  if (tid < head) put(tid, as_f32(src[tid]));
+  const uint4* vsrc = reinterpret_cast<const uint4*>(src + head);
+  constexpr int kAhead = 4;
+  for (int v0 = 0; v0 < vecs; v0 += kSThreads * kAhead) {
+    uint4 w[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int v = v0 + j * kSThreads + tid;
+      if (v < vecs) w[j] = __ldcs(vsrc + v);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int v = v0 + j * kSThreads + tid;
+      if (v < vecs) {
+        const T* e = reinterpret_cast<const T*>(&w[j]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) put(head + v * kVec + i, as_f32(e[i]));
+      }
+    }
+  }
+  for (int i = head + vecs * kVec + tid; i < n; i += kSThreads) put(i, as_f32(src[i]));
+  for (int i = tid; i < 256; i += kSThreads) s.pow2[i] = make_float2(g_pow2.hi[i], g_pow2.lo[i]);
+
+  const float T0 = a.temperature ? a.temperature[row] : 1.f;
+  const int k0 = a.top_k ? a.top_k[row] : 0;
+  const float p0 = a.top_p ? a.top_p[row] : 1.f, q0 = a.min_p ? a.min_p[row] : 0.f;
+  const float u0 = a.u[row];
+
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s.wmax[warp] = top;
+  __syncthreads();
+  if (tid == 0) {
+    float v = s.wmax[0];
+    for (int w = 1; w < kSWarps; ++w) v = fmaxf(v, s.wmax[w]);
+    s.cmax = v;
+    s.cfirst = 0xFFFFFFFFu;
+  }
+  cluster.sync();
+  float m = -INFINITY;
+  for (int r = 0; r < C; ++r) m = fmaxf(m, cluster.map_shared_rank(&s, r)->cmax);
+
+  if (m == -INFINITY) {
+    if (rank == 0 && tid == 0) {
+      a.tokens[row] = -1;
+      if (a.probs) a.probs[row] = 0.f;
+    }
+    cluster.sync();  // no CTA leaves while another may read its sums
+    return;
+  }
+  if (!(T0 > 0.f) || k0 == 1 || p0 <= 0.f || q0 > 1.f) {  // greedy, or only the first of the order is kept
+    uint32_t first = 0xFFFFFFFFu;
+    for (int i = tid; i < n; i += kSThreads)
+      if (z[i] == m) first = min(first, base + i);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0 && first != 0xFFFFFFFFu) atomicMin(&s.cfirst, first);
+    cluster.sync();
+    if (rank == 0 && tid == 0) {
+      for (int r = 0; r < C; ++r) first = min(first, cluster.map_shared_rank(&s, r)->cfirst);
+      a.tokens[row] = (int32_t)first;
+      if (a.probs) a.probs[row] = 1.f;
+    }
+    cluster.sync();
+    return;
+  }
+  if (m == INFINITY) {  // infinite logits share the weight
+    for (int i = tid; i < n; i += kSThreads) z[i] = z[i] == INFINITY ? 0.f : -INFINITY;
+    m = 0.f;
+    __syncthreads();
+  }
+  const Slice v{z, n, base, m, rate_of(fminf(fmaxf(T0, 1e-30f), 1e30f))};
+
+  Cut cut{0, 0xFFFFFFFFu};
+  bool limited = false;
+  if (k0 > 1 && k0 < a.vocab) {
+    find_cut(cluster, s, s0, v, cut, false, false, (uint32_t)k0, 0);
+    cut = s0->cut;
+    limited = true;
+    cluster.sync();
+  }
+  // each warp's contiguous share of the slice: its kept mass in wsum, the CTA's in ctotal
+  const int seg = (n + kSWarps - 1) / kSWarps, lo = min(warp * seg, n), hi = min(lo + seg, n);
+  auto kept_weight = [&](int i, uint64_t least) -> uint64_t {
+    if (i >= hi || (limited && !kept(key_of(z[i]), base + i, cut))) return 0;
+    const uint64_t w = weight(z[i], m, v.c, s.pow2);
+    return w >= least ? w : 0;
+  };
+  auto sum_kept = [&](uint64_t least) {
+    uint64_t sum = 0;
+    for (int i = lo + lane; i < hi; i += 32) sum += kept_weight(i, least);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncthreads();
+    if (lane == 0) s.wsum[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      uint64_t all = 0;
+      for (int w = 0; w < kSWarps; ++w) all += s.wsum[w];
+      s.ctotal = all;
+    }
+    cluster.sync();
+  };
+  if (p0 < 1.f) {
+    sum_kept(0);
+    uint64_t total = 0;
+    for (int r = 0; r < C; ++r) total += cluster.map_shared_rank(&s, r)->ctotal;
+    // front < total * p  <=>  front < ceil(total * p)
+    find_cut(cluster, s, s0, v, cut, limited, true, 0, max(mul_frac(total, p0, true), (uint64_t)1));
+    cut = s0->cut;
+    limited = true;
+    cluster.sync();
+  }
+  const uint64_t least = q0 > 0.f ? (q0 >= 1.f ? 1ull << kUnit : mul_frac(1ull << kUnit, q0, true)) : 0;
+  sum_kept(least);
+  uint64_t total = 0, front = 0;
+  for (int r = 0; r < C; ++r) {
+    const uint64_t t = cluster.map_shared_rank(&s, r)->ctotal;
+    if (r < rank) front += t;
+    total += t;
+  }
+  for (int w = 0; w < warp; ++w) front += s.wsum[w];
+  // sum > u * total  <=>  sum > floor(u * total)
+  const uint64_t at = mul_frac(total, u0 > 0.f ? fminf(u0, 0.99999994f) : 0.f, false);
+  if (front <= at && at < front + s.wsum[warp]) {
+    for (int i0 = lo; i0 < hi && front <= at; i0 += 32) {
+      const uint64_t w = kept_weight(i0 + lane, least);
+      uint64_t incl = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (front + incl - w <= at && at < front + incl) {
+        a.tokens[row] = (int32_t)(base + i0 + lane);
+        if (a.probs) a.probs[row] = (float)w / (float)total;
+      }
+      front += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  cluster.sync();
+}
+
+template <typename T>
+moe_status_t launch_sample(SampleArgs a, cudaStream_t st) {
+  int sms = 0;
+  const moe_status_t ok = device_sms(&sms);
+  if (ok != MOE_OK) return ok;
+  // Slices of at most 80 KB leave room for two CTAs an SM; few rows take larger
+  // clusters, down to slices of 4,096, so that one row's read and passes are
+  // spread over more SMs.
+  int C = 1;
+  while (C < kMaxCluster && (a.vocab + C - 1) / C > 20480) C *= 2;
+  while (C < kMaxCluster && (int64_t)a.rows * C * 2 <= sms && a.vocab / C > 4096) C *= 2;
+  a.slice = (((a.vocab + C - 1) / C) + 7) & ~7;
+  const int smem = (int)sizeof(Shared) + a.slice * 4;
+  if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.rows * C));
+  cfg.blockDim = dim3(kSThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = C;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" MOE_API moe_status_t moe_sample(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
+                                           const float* u, const float* temperature, const int32_t* top_k,
+                                           const float* top_p, const float* min_p, int32_t* tokens, float* probs,
+                                           void* cuda_stream) {
+  if (dtype != MOE_BF16 && dtype != MOE_FP16 && dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  const int size = dtype == MOE_FP32 ? 4 : 2;
+  if (rows < 0 || vocab < 1 || row_stride < 0 || (rows > 1 && row_stride < vocab)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!logits || !u || !tokens || ((uintptr_t)logits % size) || ((uintptr_t)u & 3) || ((uintptr_t)temperature & 3) ||
+      ((uintptr_t)top_k & 3) || ((uintptr_t)top_p & 3) || ((uintptr_t)min_p & 3) || ((uintptr_t)tokens & 3) ||
+      ((uintptr_t)probs & 3))
+    return MOE_ERR_INVALID_ARG;
+  if (vocab > moe::kMaxVocab || rows > 1 << 28) return MOE_ERR_UNSUPPORTED;
+  const moe::SampleArgs a{logits, row_stride, rows, vocab, 0, u, temperature, top_p, min_p, top_k, tokens, probs};
+  const cudaStream_t s = (cudaStream_t)cuda_stream;
+  if (dtype == MOE_FP32) return moe::launch_sample<float>(a, s);
+  if (dtype == MOE_BF16) return moe::launch_sample<__nv_bfloat16>(a, s);
+  return moe::launch_sample<__half>(a, s);
+}

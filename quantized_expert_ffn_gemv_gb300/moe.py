@@ -1,7 +1,8 @@
-"""ctypes binding of the CUDA library (include/moe.h).
+"""ctypes binding of the CUDA library (include/moe.h, include/moe_model.h).
 
 Argument marshalling only: every step of the layer runs in the library's
-kernels.  Functions mirror the C ABI names; ``MoeLayer`` bundles one layer
+kernels.  The calls of moe_model.h have their Python side in ``attention``
+and ``sampling``.  Functions mirror the C ABI names; ``MoeLayer`` bundles one layer
 handle with the torch tensors whose lifetime it needs (router weights, slot
 arena).  There is no CPU fallback: a missing library or GPU raises.
 """
@@ -19,7 +20,8 @@ EXPORTS = ["moe_expert_bytes", "moe_repack_expert", "moe_unpack_expert", "moe_la
            "moe_slot_pool_configure", "moe_forward", "moe_residual_rmsnorm", "moe_get_stats", "moe_get_miss_log",
            "moe_set_wait_timeout_ns", "moe_debug_copy_faults", "moe_destroy", "moe_status_string",
            "moe_route_noalloc", "moe_set_miss_service", "moe_slot_pool_seed", "moe_forward_norm",
-           "moe_set_next_layer"]
+           "moe_set_next_layer", "moe_rope_table", "moe_qk_norm_rope", "moe_kv_page_bytes", "moe_kv_append",
+           "moe_kv_append_norm_rope", "moe_kv_read", "moe_kv_attend_workspace", "moe_kv_attend", "moe_sample"]
 
 
 class MoeError(RuntimeError):
@@ -38,6 +40,26 @@ class LayerDesc(C.Structure):
 class Stats(C.Structure):
     _fields_ = [("forwards", C.c_uint64), ("hits", C.c_uint64), ("misses", C.c_uint64), ("h2d_bytes", C.c_uint64),
                 ("wait_ns", C.c_uint64), ("n_slots", C.c_int32), ("error", C.c_int32), ("rechecks", C.c_uint64)]
+
+
+class Heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class NormRope(C.Structure):
+    _fields_ = [("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("table", C.c_void_p), ("n_positions", C.c_int32),
+                ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("eps", C.c_float), ("weight_offset", C.c_float)]
+
+
+class KvCacheDesc(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("data_bytes", C.c_size_t), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("bits", C.c_int32), ("status", C.c_void_p)]
+
+
+class KvBatchDesc(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("seq_lens", C.c_void_p), ("cu_tokens", C.c_void_p), ("n_seqs", C.c_int32),
+                ("table_stride", C.c_int32), ("max_pages", C.c_int32), ("n_tokens", C.c_int32),
+                ("max_tokens", C.c_int32)]
 
 
 _lib = None
@@ -73,10 +95,21 @@ def lib(build_if_missing=False):
         L.moe_destroy.argtypes = [p]
         L.moe_destroy.restype = None
         L.moe_route_noalloc.argtypes = [p, p, p, i32, i32, i32, i32, p, p, p]
+        heads, norm, cache, batch = (C.POINTER(x) for x in (Heads, NormRope, KvCacheDesc, KvBatchDesc))
+        L.moe_rope_table.argtypes = [i32, i32, C.c_double, p]
+        L.moe_qk_norm_rope.argtypes = [norm, i32, i32, i32, i32, heads, heads, i32, heads, heads, p, p]
+        L.moe_kv_page_bytes.argtypes = [i32, i32, i32, i32]
+        L.moe_kv_page_bytes.restype = C.c_size_t
+        L.moe_kv_append.argtypes = [cache, batch, i32, heads, heads, p]
+        L.moe_kv_append_norm_rope.argtypes = [cache, batch, norm, i32, i32, heads, heads, heads, heads, p, p]
+        L.moe_kv_read.argtypes = [cache, batch, i32, heads, heads, p]
+        L.moe_kv_attend_workspace.argtypes = [cache, batch, i32, i32, C.POINTER(C.c_size_t)]
+        L.moe_kv_attend.argtypes = [cache, batch, i32, i32, heads, heads, p, C.c_float, i32, p, C.c_size_t, p]
+        L.moe_sample.argtypes = [p, i32, i32, i32, i64, p, p, p, p, p, p, p, p]
         L.moe_status_string.argtypes = [C.c_int]
         L.moe_status_string.restype = C.c_char_p
         for f in EXPORTS:
-            if f not in ("moe_destroy", "moe_status_string", "moe_expert_bytes"):
+            if f not in ("moe_destroy", "moe_status_string", "moe_expert_bytes", "moe_kv_page_bytes"):
                 getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
