@@ -210,7 +210,7 @@ MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_bat
  *   token  the first kept index, ascending, at which the running sum of w
  *          exceeds u times the kept sum
  * temperature <= 0 is greedy: the first of the order.  A NaN parameter is
- * taken as off (temperature: greedy).  Weights are evaluated to about 2^-32
+ * taken as off (temperature: greedy).  Weights are evaluated to about 2^-31
  * relative and summed as integers (units of 2^-45 of the largest), so results
  * do not depend on the order of execution.  Temperatures are clamped to
  * 1e-30..1e30.  A maximum of +infinity: equal weight for every infinite

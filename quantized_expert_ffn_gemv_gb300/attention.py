@@ -6,88 +6,107 @@ here, so a mismatched tensor is a ValueError and never an out-of-bounds device
 access; the contents of the batch's index arrays are checked on the device
 (``KvCache.check``).  Calls run on ``stream``, or on the current stream of the
 tensors' device; tensors they return are allocated there.
+
+A decode step makes several of these calls a layer, so each function first
+offers its arguments to the extension module (csrc/binding.c), which makes
+the same checks natively and declines (None) whatever is not the plain case; what
+follows it here takes the rest and names what is wrong.
 """
-import contextlib
 import ctypes as C
+import importlib.util
+import os
 
 import numpy as np
+import torch
 
+from . import build as _build
 from . import moe
 
 BAD_PAGE, BAD_BATCH, TIMEOUT = 1, 2, 4
 
+_HALF = {torch.bfloat16: 0, torch.float16: 1}
+_i32, _f32 = torch.int32, torch.float32
+_heads2, _heads4 = C.c_int64 * 6, C.c_int64 * 12  # two and four moe_heads_t side by side, 24 bytes each
+_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
 
-def _torch():
-    import torch
-    return torch
+
+def _load_native():
+    """The extension module, bound to the library's functions."""
+    if not os.path.exists(_build.BINDING):
+        raise RuntimeError(f"extension module not built ({_build.BINDING}); run __graft_entry__.build()")
+    spec = importlib.util.spec_from_file_location("moe_binding", _build.BINDING)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    L = moe.lib()
+    names = ("moe_qk_norm_rope", "moe_kv_append", "moe_kv_append_norm_rope", "moe_kv_read", "moe_kv_attend_workspace",
+             "moe_kv_attend", "moe_sample")
+    m.setup(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in names),
+            (torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8), torch._C._cuda_getDevice,
+            _raw_stream, torch.empty)
+    return m
 
 
-_HALF = {}  # torch.bfloat16 / torch.float16 -> the library's code (filled on first use: torch is imported lazily)
+_native_module = None
+
+
+def _native():
+    global _native_module
+    if _native_module is None:
+        _native_module = _load_native()
+    return _native_module
 
 
 def _code(dtype, name):
-    if not _HALF:
-        torch = _torch()
-        _HALF.update({torch.bfloat16: 0, torch.float16: 1})
     code = _HALF.get(dtype)
     if code is None:
         raise ValueError(f"{name}: expected torch.bfloat16 or torch.float16, got {dtype}")
     return code
 
 
-def _scope(device, stream):
-    """Raw stream to launch on, and a context in which `device` is current and allocations belong to the stream."""
-    torch = _torch()
+def _scope(dev, stream):
+    """A context in which device number dev and, when given, the stream are
+    current; None when they are already."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        return stream.cuda_stream, torch.cuda.stream(stream)
-    raw = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
-        return raw, contextlib.nullcontext()
-    return raw, torch.cuda.device(device)
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        return torch.cuda.stream(stream)
+    return None if _current_device() == dev else torch.cuda.device(dev)
 
 
-def _on_gpu(t, name, device=None):
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor{'' if device is None else f' on {device}'}, got {t.device}")
-    return t.device
+def _on_gpu(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return dev
 
 
-def _rows(t, name, shape, dtype, device, out=False):
-    """The library's view of a [tokens, heads, D] tensor."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    ts, hs, es = t.stride()
-    if es != 1 or (ts | hs) & 7 or t.data_ptr() & 15:
-        raise ValueError(f"{name}: heads must be contiguous, strides multiples of 8 elements and data 16-byte aligned")
-    if out and ((shape[0] > 1 and ts < shape[2]) or (shape[1] > 1 and hs < shape[2])):
-        raise ValueError(f"{name}: rows of an output must not overlap")
-    return moe.Heads(t.data_ptr(), ts, hs)
+def _rows(t, name, shape, dtype, dev, out=False):
+    """Address and strides of a [tokens, heads, D] tensor, checked."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
+        ts, hs, es = t.stride()
+        at = t.data_ptr()
+        if es != 1 or (ts | hs) & 7 or at & 15:
+            raise ValueError(f"{name}: heads must be contiguous, strides multiples of 8 elements and data 16-byte aligned")
+        if out and ((shape[0] > 1 and ts < shape[2]) or (shape[1] > 1 and hs < shape[2])):
+            raise ValueError(f"{name}: rows of an output must not overlap")
+        return at, ts, hs
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}, got {t.device}")
 
 
-def _out(t, name, shape, dtype, device):
-    """An output given by the caller, checked; or a new one."""
-    if t is None:
-        t = _torch().empty(shape, dtype=dtype, device=device)
-    return t, _rows(t, name, shape, dtype, device, True)
-
-
-def _vector(t, name, dtype, n, device):
+def _vector(t, name, dtype, n, dev):
+    """Address of a contiguous [n] tensor, checked; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} ({n},), got {t.dtype} {tuple(t.shape)}")
-    _on_gpu(t, name, device)
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == (n,) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected contiguous {dtype} ({n},) on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def rope_table(n_positions, rot_dim, base, device="cuda"):
     """cos and sin of position * base^(-2 i / rot_dim), angles in 64 bits:
     float32 [n_positions, rot_dim / 2, 2] on `device`."""
-    torch = _torch()
     if n_positions < 1 or rot_dim < 16 or rot_dim % 16:
         raise ValueError("n_positions must be positive and rot_dim a positive multiple of 16")
     t = np.empty((n_positions, rot_dim // 2, 2), np.float32)
@@ -95,16 +114,18 @@ def rope_table(n_positions, rot_dim, base, device="cuda"):
     return torch.from_numpy(t).to(device)
 
 
-def _norm_rope(dtype, dim, device, table, q_weight, k_weight, eps, interleaved, weight_offset):
-    torch = _torch()
-    n_positions = rot = ptr = 0
+def _norm_rope(dtype, dim, dev, table, q_weight, k_weight, eps, interleaved, weight_offset):
+    n_positions = rot = 0
+    at = None
     if table is not None:
-        if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
+        shape = table.shape
+        if table.dtype is not _f32 or len(shape) != 3 or shape[2] != 2 or not table.is_contiguous():
             raise ValueError("table: expected contiguous float32 [n_positions, rot_dim / 2, 2]")
-        _on_gpu(table, "table", device)
-        n_positions, rot, ptr = table.shape[0], 2 * table.shape[1], table.data_ptr()
-    return moe.NormRope(_vector(q_weight, "q_weight", dtype, dim, device), _vector(k_weight, "k_weight", dtype, dim, device),
-                        ptr, n_positions, rot, int(bool(interleaved)), eps, weight_offset)
+        if table.get_device() != dev:
+            raise ValueError(f"table must be a CUDA tensor on cuda:{dev}, got {table.device}")
+        n_positions, rot, at = shape[0], 2 * shape[1], table.data_ptr()
+    return moe.NormRope(_vector(q_weight, "q_weight", dtype, dim, dev), _vector(k_weight, "k_weight", dtype, dim, dev), at,
+                        n_positions, rot, 1 if interleaved else 0, eps, weight_offset)
 
 
 def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, weight_offset=0.0,
@@ -114,23 +135,37 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6,
     are taken as they are).  table: as rope_table gives it, or None for the
     norm alone; positions: int32 [T].  Returns (q_out, k_out); q_out may be q
     and k_out k.  See moe_qk_norm_rope."""
-    torch = _torch()
+    if stream is None:
+        r = (_native_module or _native()).qk_norm_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, weight_offset,
+                                                       q_out, k_out)
+        if r is not None:
+            return r if type(r) is tuple else moe.check(r, "moe_qk_norm_rope")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [T, heads, D]")
-    T, nq, dim = q.shape
+    T, nq, dim = q_shape = q.shape
     nk = k.shape[1]
-    dev, dtype = _on_gpu(q, "q"), q.dtype
+    k_shape = (T, nk, dim)
+    dtype = q.dtype
     code = _code(dtype, "q")
     if table is not None and positions is None:
         raise ValueError("a rotation needs positions")
+    dev = _on_gpu(q, "q")
+    scope = _scope(dev, stream)
+    if scope is not None:
+        with scope:
+            return qk_norm_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, weight_offset, q_out, k_out)
     desc = _norm_rope(dtype, dim, dev, table, q_weight, k_weight, eps, interleaved, weight_offset)
-    qh, kh = _rows(q, "q", (T, nq, dim), dtype, dev), _rows(k, "k", (T, nk, dim), dtype, dev)
-    pos = _vector(positions, "positions", torch.int32, T, dev)
-    raw, scope = _scope(dev, stream)
-    with scope:
-        q_out, qo = _out(q_out, "q_out", (T, nq, dim), dtype, dev)
-        k_out, ko = _out(k_out, "k_out", (T, nk, dim), dtype, dev)
-        moe.check(moe.lib().moe_qk_norm_rope(desc, code, T, dim, nq, qh, qo, nk, kh, ko, pos, raw), "moe_qk_norm_rope")
+    qr, kr = _rows(q, "q", q_shape, dtype, dev), _rows(k, "k", k_shape, dtype, dev)
+    pos = _vector(positions, "positions", _i32, T, dev)
+    if q_out is None:
+        q_out = q.new_empty(q_shape)
+    if k_out is None:
+        k_out = k.new_empty(k_shape)
+    h = _heads4(*qr, *kr, *_rows(q_out, "q_out", q_shape, dtype, dev, True), *_rows(k_out, "k_out", k_shape, dtype, dev, True))
+    at = C.addressof(h)
+    code = moe.lib().moe_qk_norm_rope(C.addressof(desc), code, T, dim, nq, at, at + 48, nk, at + 24, at + 72, pos, _raw_stream(dev))
+    if code:
+        moe.check(code, "moe_qk_norm_rope")
     return q_out, k_out
 
 
@@ -143,11 +178,10 @@ class KvBatch:
     when a call runs."""
 
     def __init__(self, block_table, seq_lens, cu_tokens, n_tokens, max_tokens=None):
-        torch = _torch()
-        if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.stride(1) != 1:
+        if block_table.dim() != 2 or block_table.dtype is not _i32 or block_table.stride(1) != 1:
             raise ValueError("block_table: expected int32 [n_seqs, max_pages] with contiguous rows")
         n_seqs, max_pages = block_table.shape
-        self.device = _on_gpu(block_table, "block_table")
+        dev = _on_gpu(block_table, "block_table")
         stride = block_table.stride(0) if n_seqs > 1 else max(block_table.stride(0), max_pages)
         if n_seqs < 1 or max_pages < 1 or stride < max_pages:
             raise ValueError("block_table: rows must not overlap, and there must be a page and a sequence")
@@ -156,10 +190,11 @@ class KvBatch:
         if n_tokens < 0 or (n_tokens and not 1 <= max_tokens <= n_tokens):
             raise ValueError("max_tokens must lie in 1..n_tokens")
         self._tensors = (block_table, seq_lens, cu_tokens)
-        self.n_seqs, self.n_tokens, self.max_tokens = n_seqs, n_tokens, max_tokens
-        self.desc = moe.KvBatchDesc(block_table.data_ptr(), _vector(seq_lens, "seq_lens", torch.int32, n_seqs, self.device),
-                                    _vector(cu_tokens, "cu_tokens", torch.int32, n_seqs + 1, self.device), n_seqs, stride,
-                                    max_pages, n_tokens, max_tokens)
+        self.dev, self.n_seqs, self.n_tokens, self.max_tokens = dev, n_seqs, n_tokens, max_tokens
+        self.desc = moe.KvBatchDesc(block_table.data_ptr(), _vector(seq_lens, "seq_lens", _i32, n_seqs, dev),
+                                    _vector(cu_tokens, "cu_tokens", _i32, n_seqs + 1, dev), n_seqs, stride, max_pages, n_tokens,
+                                    max_tokens)
+        self._at = C.addressof(self.desc)
 
 
 class KvCache:
@@ -170,7 +205,6 @@ class KvCache:
     or None to allocate one."""
 
     def __init__(self, n_pages, page_size, n_kv_heads, head_dim, bits=8, device=0, data=None):
-        torch = _torch()
         page = int(moe.lib().moe_kv_page_bytes(page_size, n_kv_heads, head_dim, bits))
         if not page or n_pages < 1:
             raise ValueError("page_size a multiple of 32 up to 4096, head_dim 64, 128 or 256, bits 8 or 4, n_pages >= 1")
@@ -178,63 +212,96 @@ class KvCache:
         self.n_kv_heads, self.head_dim, self.bits = n_kv_heads, head_dim, bits
         if data is None:
             data = torch.empty(n_pages * page, dtype=torch.uint8, device=torch.device("cuda", device))
-        elif data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != n_pages * page or data.data_ptr() & 15:
+        elif data.dtype is not torch.uint8 or not data.is_contiguous() or data.numel() != n_pages * page or data.data_ptr() & 15:
             raise ValueError(f"data: expected {n_pages * page} contiguous 16-byte aligned uint8")
-        self.device = _on_gpu(data, "data")
+        self.dev = _on_gpu(data, "data")
         self.data = data
-        self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._status = torch.zeros(1, dtype=_i32, device=data.device)
         self.desc = moe.KvCacheDesc(data.data_ptr(), data.numel(), n_pages, page_size, n_kv_heads, head_dim, bits,
                                     self._status.data_ptr())
+        self._at = C.addressof(self.desc)
 
-    def _io(self, batch, stream):
-        if batch.device != self.device:
-            raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
-        return _scope(self.device, stream)
+    def _enter(self, batch, stream):
+        if batch.dev != self.dev:
+            raise ValueError(f"the batch is on cuda:{batch.dev}, the cache on cuda:{self.dev}")
+        return _scope(self.dev, stream)
 
     def append(self, k, v, batch, stream=None):
         """Quantise the batch's new k, v [n_tokens, n_kv_heads, head_dim] into their pages (moe_kv_append)."""
-        shape, dtype = (batch.n_tokens, self.n_kv_heads, self.head_dim), k.dtype
+        if stream is None and batch.dev == self.dev:
+            r = (_native_module or _native()).append(self._at, batch._at, self.dev, k, v)
+            if r is not None:
+                return moe.check(r, "moe_kv_append") if r else None
+        shape, dtype, dev = (batch.n_tokens, self.n_kv_heads, self.head_dim), k.dtype, self.dev
         code = _code(dtype, "k")
-        kh, vh = _rows(k, "k", shape, dtype, self.device), _rows(v, "v", shape, dtype, self.device)
-        raw, scope = self._io(batch, stream)
-        with scope:
-            moe.check(moe.lib().moe_kv_append(self.desc, batch.desc, code, kh, vh, raw), "moe_kv_append")
+        h = _heads2(*_rows(k, "k", shape, dtype, dev), *_rows(v, "v", shape, dtype, dev))
+        scope = self._enter(batch, stream)
+        if scope is not None:
+            with scope:
+                return self.append(k, v, batch)
+        at = C.addressof(h)
+        code = moe.lib().moe_kv_append(self._at, batch._at, code, at, at + 24, _raw_stream(dev))
+        if code:
+            moe.check(code, "moe_kv_append")
 
     def append_norm_rope(self, q, k, v, batch, table, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                          weight_offset=0.0, positions=None, q_out=None, stream=None):
         """qk_norm_rope of q and k, and append of the result and v, in one
         pass; positions default to the tokens' places in their sequences.
         Returns q_out (may be q).  See moe_kv_append_norm_rope."""
-        torch = _torch()
-        dtype, T = q.dtype, batch.n_tokens
+        if stream is None and batch.dev == self.dev:
+            r = (_native_module or _native()).append_norm_rope(self._at, batch._at, self.dev, q, k, v, table, q_weight, k_weight,
+                                                               eps, interleaved, weight_offset, positions, q_out)
+            if r is not None:
+                return moe.check(r, "moe_kv_append_norm_rope") if type(r) is int else r
         if q.dim() != 3:
             raise ValueError("q must be [n_tokens, heads, head_dim]")
-        nq, kv = q.shape[1], (T, self.n_kv_heads, self.head_dim)
+        dtype, T, dim, dev = q.dtype, batch.n_tokens, self.head_dim, self.dev
         code = _code(dtype, "q")
-        desc = _norm_rope(dtype, self.head_dim, self.device, table, q_weight, k_weight, eps, interleaved, weight_offset)
-        qh = _rows(q, "q", (T, nq, self.head_dim), dtype, self.device)
-        kh, vh = _rows(k, "k", kv, dtype, self.device), _rows(v, "v", kv, dtype, self.device)
-        pos = _vector(positions, "positions", torch.int32, T, self.device)
-        raw, scope = self._io(batch, stream)
-        with scope:
-            q_out, qo = _out(q_out, "q_out", (T, nq, self.head_dim), dtype, self.device)
-            moe.check(moe.lib().moe_kv_append_norm_rope(self.desc, batch.desc, desc, code, nq, qh, qo, kh, vh, pos, raw),
-                      "moe_kv_append_norm_rope")
+        nq = q.shape[1]
+        q_shape, kv = (T, nq, dim), (T, self.n_kv_heads, dim)
+        qr, kr, vr = _rows(q, "q", q_shape, dtype, dev), _rows(k, "k", kv, dtype, dev), _rows(v, "v", kv, dtype, dev)
+        scope = self._enter(batch, stream)
+        if scope is not None:
+            with scope:
+                return self.append_norm_rope(q, k, v, batch, table, q_weight, k_weight, eps, interleaved, weight_offset,
+                                             positions, q_out)
+        desc = _norm_rope(dtype, dim, dev, table, q_weight, k_weight, eps, interleaved, weight_offset)
+        pos = _vector(positions, "positions", _i32, T, dev)
+        if q_out is None:
+            q_out = q.new_empty(q_shape)
+        h = _heads4(*qr, *_rows(q_out, "q_out", q_shape, dtype, dev, True), *kr, *vr)
+        at = C.addressof(h)
+        code = moe.lib().moe_kv_append_norm_rope(self._at, batch._at, C.addressof(desc), code, nq, at, at + 24, at + 48, at + 72,
+                                                 pos, _raw_stream(dev))
+        if code:
+            moe.check(code, "moe_kv_append_norm_rope")
         return q_out
 
     def read(self, batch, k_out=None, v_out=None, dtype=None, stream=None):
         """The batch's tokens back from the cache, (k, v) [n_tokens,
         n_kv_heads, head_dim] in dtype (default bf16, or k_out's).  See moe_kv_read."""
-        torch = _torch()
         if dtype is None:
             dtype = torch.bfloat16 if k_out is None else k_out.dtype
-        shape = (batch.n_tokens, self.n_kv_heads, self.head_dim)
+        if stream is None and batch.dev == self.dev:
+            r = (_native_module or _native()).read(self._at, batch._at, self.dev, self.data, dtype, k_out, v_out)
+            if r is not None:
+                return r if type(r) is tuple else moe.check(r, "moe_kv_read")
         code = _code(dtype, "dtype")
-        raw, scope = self._io(batch, stream)
-        with scope:
-            k_out, ko = _out(k_out, "k_out", shape, dtype, self.device)
-            v_out, vo = _out(v_out, "v_out", shape, dtype, self.device)
-            moe.check(moe.lib().moe_kv_read(self.desc, batch.desc, code, ko, vo, raw), "moe_kv_read")
+        dev, shape = self.dev, (batch.n_tokens, self.n_kv_heads, self.head_dim)
+        scope = self._enter(batch, stream)
+        if scope is not None:
+            with scope:
+                return self.read(batch, k_out, v_out, dtype)
+        if k_out is None:
+            k_out = self.data.new_empty(shape, dtype=dtype)
+        if v_out is None:
+            v_out = self.data.new_empty(shape, dtype=dtype)
+        h = _heads2(*_rows(k_out, "k_out", shape, dtype, dev, True), *_rows(v_out, "v_out", shape, dtype, dev, True))
+        at = C.addressof(h)
+        code = moe.lib().moe_kv_read(self._at, batch._at, code, at, at + 24, _raw_stream(dev))
+        if code:
+            moe.check(code, "moe_kv_read")
         return k_out, v_out
 
     def attend(self, q, batch, scale=None, out=None, lse=None, shared_tokens=0, stream=None):
@@ -245,29 +312,39 @@ class KvCache:
         positions (a multiple of page_size) whose pages are the same in every
         row of the block table; they are then read once for the whole batch.
         Returns out.  See moe_kv_attend."""
-        torch = _torch()
+        if stream is None and batch.dev == self.dev:
+            r = (_native_module or _native()).attend(self._at, batch._at, self.dev, self.data, q, scale, out, lse, shared_tokens)
+            if r is not None:
+                return moe.check(r, "moe_kv_attend") if type(r) is int else r
         if q.dim() != 3:
             raise ValueError("q must be [n_tokens, heads, head_dim]")
-        dtype, T, nq = q.dtype, batch.n_tokens, q.shape[1]
-        shape = (T, nq, self.head_dim)
+        dtype, T, nq, dim, dev = q.dtype, batch.n_tokens, q.shape[1], self.head_dim, self.dev
+        shape = (T, nq, dim)
         code = _code(dtype, "q")
-        qh = _rows(q, "q", shape, dtype, self.device)
-        lse_ptr = None
+        qr = _rows(q, "q", shape, dtype, dev)
+        lse_at = None
         if lse is not None:
-            if lse.dtype != torch.float32 or tuple(lse.shape) != (T, nq) or not lse.is_contiguous():
-                raise ValueError(f"lse: expected contiguous float32 {(T, nq)}")
-            _on_gpu(lse, "lse", self.device)
-            lse_ptr = lse.data_ptr()
-        raw, scope = self._io(batch, stream)
-        with scope:
-            out, oh = _out(out, "out", shape, dtype, self.device)
-            n = C.c_size_t()
-            L = moe.lib()
-            moe.check(L.moe_kv_attend_workspace(self.desc, batch.desc, nq, shared_tokens, n), "moe_kv_attend_workspace")
-            work = torch.empty(n.value, dtype=torch.uint8, device=self.device)
-            moe.check(L.moe_kv_attend(self.desc, batch.desc, code, nq, qh, oh, lse_ptr,
-                                      self.head_dim ** -0.5 if scale is None else scale, shared_tokens, work.data_ptr(),
-                                      n.value, raw), "moe_kv_attend")
+            if lse.dtype is not _f32 or lse.shape != (T, nq) or lse.get_device() != dev or not lse.is_contiguous():
+                raise ValueError(f"lse: expected contiguous float32 {(T, nq)} on cuda:{dev}")
+            lse_at = lse.data_ptr()
+        scope = self._enter(batch, stream)
+        if scope is not None:
+            with scope:
+                return self.attend(q, batch, scale, out, lse, shared_tokens)
+        if out is None:
+            out = q.new_empty(shape)
+        h = _heads2(*qr, *_rows(out, "out", shape, dtype, dev, True))
+        at = C.addressof(h)
+        n = C.c_size_t()
+        L = moe.lib()
+        status = L.moe_kv_attend_workspace(self._at, batch._at, nq, shared_tokens, C.addressof(n))
+        if status:
+            moe.check(status, "moe_kv_attend_workspace")
+        work = self.data.new_empty(n.value)
+        status = L.moe_kv_attend(self._at, batch._at, code, nq, at, at + 24, lse_at, dim ** -0.5 if scale is None else scale,
+                                 shared_tokens, work.data_ptr(), n.value, _raw_stream(dev))
+        if status:
+            moe.check(status, "moe_kv_attend")
         return out
 
     def check(self):

@@ -1,15 +1,19 @@
 """In-tree build of the package's native libraries.
 
 - libmoe_synth.so: the seeded input generator (plain C, gcc).
-- libmoe_gb300.so: the CUDA library behind include/moe.h (nvcc, sm_103a only).
+- libmoe_gb300.so: the CUDA library behind include/moe.h and
+  include/moe_model.h (nvcc, sm_103a only).
+- moe_binding.so: the Python extension with the short path of the binding of
+  moe_model.h (plain C against the CPython API, gcc).
 
-Both land in quantized_expert_ffn_gemv_gb300/_build/ (git-ignored).  Sources are
+All land in quantized_expert_ffn_gemv_gb300/_build/ (git-ignored).  Sources are
 recompiled when they are newer than the library.
 """
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 SYNTH_LIB = os.path.join(OUT, "libmoe_synth.so")
 CUDA_LIB = os.path.join(OUT, "libmoe_gb300.so")
+BINDING = os.path.join(OUT, "moe_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -38,6 +43,17 @@ def build_synth(force=False):
                         "-pthread", "-Wall", "-o", tmp, src, "-lm"], check=True)
         os.replace(tmp, SYNTH_LIB)
     return SYNTH_LIB
+
+
+def build_binding(force=False):
+    src = os.path.join(CSRC, "binding.c")
+    os.makedirs(OUT, exist_ok=True)
+    if force or _stale(BINDING, [src] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        subprocess.run(["gcc", "-O2", "-std=gnu11", "-fPIC", "-shared", "-Wall", "-I", os.path.join(ROOT, "include"), "-I",
+                        sysconfig.get_paths()["include"], "-o", tmp, src], check=True)
+        os.replace(tmp, BINDING)
+    return BINDING
 
 
 def cuda_sources():
@@ -90,7 +106,7 @@ def build_cuda(force=False, verbose=False):
 
 
 def build_all(force=False, verbose=False):
-    return build_synth(force), build_cuda(force, verbose)
+    return build_synth(force), build_binding(force), build_cuda(force, verbose)
 
 
 if __name__ == "__main__":

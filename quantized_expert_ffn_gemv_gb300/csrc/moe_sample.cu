@@ -4,19 +4,23 @@
 // the token.  With the row at hand the bound is the one read of the logits;
 // for a single row it is the chain of cluster barriers.
 //
-// Weights w = 2^-y, y = (max - z) log2(e) / T, are evaluated to about 2^-32
-// relative (float pairs for y, a 256-entry table and a cubic for the rest)
-// and held as integers in units of 2^-45: integer sums have no order, so any
-// split of the work gives the same bits, and the sums that top-p, min-p and
-// the draw compare are exact.
+// Weights w = 2^-y, y = (max - z) log2(e) / T, are evaluated to about 2^-31
+// relative (float pairs for y, a 512-entry table and a cubic for the rest)
+// and summed as integers in units of 2^-45: integer sums have no order, so
+// any split of the work gives the same bits, and the sums that top-p, min-p
+// and the draw compare are exact.  Conversions go through the float's
+// mantissa (adding 1.5 * 2^23): the conversion unit is a quarter as wide, and the 64-bit
+// one that a first version used took half of its time.
 //
 // The cut.  Kept elements are a prefix of the order (logit descending, index
 // ascending).  A histogram of y (1/16 octave a bin; counts, and masses as two
 // 16-bit halves relative to the bin's octave) finds the bin the cut falls
-// into.  If few elements share it, they are collected in the first CTA and
-// ranked exactly; otherwise the bin's range of logits is histogrammed again,
-// finer, until few are left or all have the same logit, whose cut is then an
-// index.
+// into.  Each CTA lists its elements of that bin and those in front of it.
+// If both fit one list, the first CTA ranks them all and draws the token by
+// itself; if only the bin's do, it ranks those for the cut's last element
+// and the cluster draws; otherwise the bin's range of logits is histogrammed
+// again, finer, until few are left or all have the same logit, whose cut is
+// then an index.
 #include <cooperative_groups.h>
 #include <cmath>
 
@@ -30,25 +34,27 @@ namespace {
 constexpr int kSThreads = 512, kSWarps = kSThreads / 32;
 constexpr int kBins = 1024, kPerOctave = 16;  // 64 octaves: beyond them a weight is 0 in units of 2^-45
 constexpr int kUnit = 45;                     // 2^18 weights of 2^45 fit 64 bits
-constexpr int kList = 768;                    // elements ranked exactly at most
+constexpr int kList = 768;                    // elements ranked against each other at most
+constexpr int kHalfList = kList / 2;          // what a CTA lists of either sort
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxCluster = 8;
+constexpr int kTable = 512;
 
 struct Pow2Table {
-  float hi[256], lo[256];
+  float2 v[kTable];
 };
-// 2^(-i/256) as float pairs: the exponential's power series in binary64.
+// 2^(-(i + 1) / 512) as float pairs: the exponential's power series in binary64.
 constexpr Pow2Table make_pow2() {
   Pow2Table t{};
-  for (int i = 0; i < 256; ++i) {
-    const double x = -0.69314718055994530942 * i / 256.0;
+  for (int i = 0; i < kTable; ++i) {
+    const double x = -0.69314718055994530942 * (i + 1) / kTable;
     double term = 1.0, sum = 1.0;
     for (int n = 1; n < 24; ++n) {
       term *= x / n;
       sum += term;
     }
-    t.hi[i] = (float)sum;
-    t.lo[i] = (float)(sum - (double)t.hi[i]);
+    t.v[i].x = (float)sum;
+    t.v[i].y = (float)(sum - (double)t.v[i].x);
   }
   return t;
 }
@@ -80,29 +86,33 @@ __device__ __forceinline__ Rate rate_of(float T) {
 __device__ __forceinline__ float y_of(float z, float m, const Rate& c) { return z == -INFINITY ? INFINITY : (m - z) * c.h; }
 __device__ __forceinline__ int bin_of(float y) { return y < 64.f ? (int)(y * kPerOctave) : kBins - 1; }
 
-// w relative to 2^-oct in units of 2^-32 (at most 2^32); 0 and oct 64 beyond 64 octaves.
-__device__ __forceinline__ uint64_t weight32(float z, float m, const Rate& c, const float2* tab, int& oct) {
+// w = W 2^-(31 + s - 1), W in 2^30 .. 2^31, s in 0 .. 64; W = 0 beyond 64 octaves.
+__device__ __forceinline__ uint32_t weight31(float z, float m, const Rate& c, const float2* tab, int& s) {
   const float yh = y_of(z, m, c);
   if (!(yh < 64.f)) {
-    oct = 64;
+    s = 64;
     return 0;
   }
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low mantissa bits are the rounded integer
   const float x = m - z, bb = x - m;
   const float xl = (m - (x - bb)) + (-z - bb);  // m - z = x + xl
   const float yl = fmaf(x, c.h, -yh) + fmaf(x, c.l, xl * c.h);
-  const float k = rintf(yh * 256.f);
-  const float r = (fmaf(k, -1.f / 256.f, yh) + yl) * 0.693147180559945f;
+  const float kf = fmaf(yh, (float)kTable, kMagic);
+  const int k = __float_as_int(kf) - 0x4B400001;  // round(512 y) - 1
+  const float r = (fmaf(kf - kMagic, -1.f / kTable, yh) + yl) * 0.693147180559945f;
   const float p = r * fmaf(r, fmaf(r, -1.f / 6.f, 0.5f), -1.f);  // e^-r - 1
-  const int ki = (int)k;
-  const float2 t = tab[ki & 255];
-  const float low = fmaf(t.x, p, t.y);
-  oct = ki >> 8;
-  return (uint64_t)((int64_t)(t.x * 4294967296.f) + (int64_t)rintf(low * 4294967296.f));
+  const float2 t = tab[k & (kTable - 1)];                        // t.x in 1/2 .. 1
+  const float low = fmaf(fmaf(t.x, p, t.y), 2147483648.f, kMagic);
+  s = (k >> 9) + 1;
+  return (((__float_as_uint(t.x) & 0x7FFFFFu) | 0x800000u) << 7) + (uint32_t)(__float_as_int(low) - 0x4B400000);
+}
+__device__ __forceinline__ uint64_t to_units(uint32_t W, int s) {
+  return s >= 64 ? 0 : (((uint64_t)W << (kUnit - 30)) + ((1ull << s) >> 1)) >> s;
 }
 __device__ __forceinline__ uint64_t weight(float z, float m, const Rate& c, const float2* tab) {
-  int oct;
-  const uint64_t w = weight32(z, m, c, tab, oct);
-  return oct >= 64 ? 0 : ((w << (kUnit - 32)) + ((1ull << oct) >> 1)) >> oct;
+  int s;
+  const uint32_t W = weight31(z, m, c, tab, s);
+  return to_units(W, s);
 }
 
 // Order-preserving image of a logit (no NaN): larger logit, larger key; -0 equals 0.
@@ -142,33 +152,40 @@ struct Cut {
 };
 __device__ __forceinline__ bool kept(uint32_t key, uint32_t idx, const Cut& c) { return key > c.key || (key == c.key && idx <= c.idx); }
 
+struct Entry {
+  uint64_t w;
+  uint32_t key, idx;
+};
+
 struct Shared {
-  // this CTA's histogram; the list of the cut bin's elements takes its place later (first CTA)
+  // this CTA's histogram, and later its lists: elements of the cut's bin, and in front of it
   union {
     struct {
       uint32_t count[kBins], hi[kBins], lo[kBins];
     } h;
-    struct {
-      uint32_t key[kList], idx[kList];
-      uint64_t w[kList];
-    } list;
+    Entry part[2][kHalfList];
   };
-  // the cluster's histogram (first CTA)
-  uint32_t mcount[kBins];
-  uint64_t mmass[kBins];
-  float2 pow2[256];
+  // first CTA: the cluster's histogram, and later the cluster's list
+  union {
+    struct {
+      uint64_t mass[kBins];
+      uint32_t count[kBins];
+    } all;
+    Entry list[kList];
+  };
+  float2 pow2[kTable];
   uint64_t wsum[kSWarps];
   uint32_t wcnt[kSWarps];
   float wmax[kSWarps];
   // written by the CTA, read by the cluster
   float cmax;
   uint32_t cfirst, ccount;  // greedy: the maximum's lowest index; find_cut: lowest and highest key, or a count
+  uint32_t part_n[2];
   uint64_t ctotal;
   // written by the first CTA, read by the cluster
-  uint32_t list_n;
   int cut_bin;
   uint32_t cut_count, cut_need;
-  uint64_t cut_before;
+  uint64_t cut_before, cut_target;
   Cut cut;
   int found;
 };
@@ -194,29 +211,109 @@ __device__ __forceinline__ void block_scan(Shared& s, uint32_t& c, uint64_t& m) 
   m = mb + mi - m;
 }
 
-// The slice of a row that a CTA holds.
+// The sum over the block's threads, for all of them.
+__device__ __forceinline__ uint64_t block_sum(Shared& s, uint64_t v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane == 0) s.wsum[warp] = v;
+  __syncthreads();
+  v = 0;
+  for (int w = 0; w < kSWarps; ++w) v += s.wsum[w];
+  return v;
+}
+
+// The slice of a row that a CTA holds, n4 float4 (the end filled with
+// -infinity), and what is asked of the row.
 struct Slice {
-  const float* z;
-  int n;
+  const float4* z;
+  int n4;
   uint32_t base;
   float m;
   Rate c;
+  uint32_t k;     // top-k, 0 = all
+  float p;        // top-p, 1 = all
+  uint64_t least; // min-p in units
+  float u;
+  int32_t* token;
+  float* prob;
 };
 
+// The first CTA alone: every element that top-k and top-p can keep is in the
+// list, n of them; cut them, and draw the token.  target: the mass that top-p
+// asks for, or 0: its share of what top-k keeps of the list.
+__device__ void draw_from_list(Shared& s, const Slice& v, int n, uint64_t target) {
+  constexpr int kPer = (kList + kSThreads - 1) / kSThreads;
+  const int tid = threadIdx.x;
+  uint64_t front[kPer], w[kPer], sum = 0;
+  uint32_t place[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = tid + j * kSThreads;
+    front[j] = w[j] = 0;
+    place[j] = 0xFFFFFFFFu;
+    if (e < n) {
+      const Entry me = s.list[e];
+      uint32_t ahead = 0;
+      for (int i = 0; i < n; ++i) {
+        const Entry o = s.list[i];
+        if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) ++ahead, front[j] += o.w;
+      }
+      place[j] = ahead;
+      w[j] = v.k > 0 && ahead >= v.k ? 0 : me.w;
+      sum += w[j];
+    }
+  }
+  if (v.p < 1.f) {
+    // front < sum * p  <=>  front < ceil(sum * p)
+    if (!target) target = max(mul_frac(block_sum(s, sum), v.p, true), (uint64_t)1);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (front[j] >= target) w[j] = 0;
+  }
+  sum = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (w[j] < v.least && place[j] != 0) w[j] = 0;
+    sum += w[j];
+  }
+  const uint64_t total = block_sum(s, sum);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (tid + j * kSThreads < n) s.list[tid + j * kSThreads].w = w[j];
+  __syncthreads();
+  // running sum > u * total  <=>  running sum > floor(u * total)
+  const uint64_t at = mul_frac(total, v.u, false);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (w[j] == 0) continue;
+    const uint32_t idx = s.list[tid + j * kSThreads].idx;
+    uint64_t below = 0;
+    for (int i = 0; i < n; ++i) below += s.list[i].idx < idx ? s.list[i].w : 0;
+    if (below <= at && at < below + w[j]) {
+      *v.token = (int32_t)idx;
+      if (v.prob) *v.prob = (float)w[j] / (float)total;
+    }
+  }
+}
+
 // The cut among the elements that `limit` keeps (all, when not limited): at
-// the need-th of the order, or, by mass, at the first where the running mass
-// reaches the target.  The whole cluster calls it; the result is in the
-// first CTA's Shared::cut afterwards, until the caller's next cluster barrier.
-__device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, const Slice& v, const Cut limit, bool limited,
-                         bool by_mass, uint32_t need, uint64_t target) {
+// the top-k'th of the order, or, by mass, at the first where the running mass
+// reaches top-p of it all.  The whole cluster calls it.  True: the token is
+// drawn.  Otherwise the cut is in the first CTA's Shared::cut until the
+// caller's next cluster barrier.
+__device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, const Slice& v, const Cut limit, bool limited,
+                         bool by_mass) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
   int level = 0, shift = 0, octave = 0, bin0 = 0;
   uint32_t top_key = 0, low_key = 0;  // level > 0: the range of keys looked at
-  uint64_t before = 0;                // mass in front of the range
-  // is element i among those looked at, and in which bin
-  auto place = [&](int i, float z, uint32_t key) -> int {
-    if (limited && !kept(key, v.base + i, limit)) return -1;
+  uint32_t need = v.k;
+  uint64_t before = 0, target = 0;  // mass in front of the range; the mass to reach (set at level 0)
+  // is an element among those looked at, and in which bin
+  auto place = [&](uint32_t idx, float z, uint32_t key) -> int {
+    if (limited && !kept(key, idx, limit)) return -1;
     const int b0 = bin_of(y_of(z, v.m, v.c));
     if (level == 0) return b0;
     return b0 == bin0 && key <= top_key && key >= low_key ? (int)((top_key - key) >> shift) : -1;
@@ -224,27 +321,28 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
   for (;;) {
     for (int i = tid; i < kBins; i += kSThreads) s.h.count[i] = s.h.hi[i] = s.h.lo[i] = 0;
     __syncthreads();
-    for (int i0 = 0; i0 < v.n; i0 += kSThreads) {
+    for (int i0 = 0; i0 < v.n4; i0 += kSThreads) {
       const int i = i0 + tid;
-      int bin = -1;
-      uint64_t w = 0;
-      if (i < v.n) {
-        const float z = v.z[i];
-        bin = place(i, z, key_of(z));
-        if (bin >= 0 && by_mass) {
-          int oct;
-          w = weight32(z, v.m, v.c, s.pow2, oct);
-          // the bin's octave is at most one below the weight's
-          w >>= min(oct - (level == 0 ? bin / kPerOctave : octave), 63);
+      const float4 q = i < v.n4 ? v.z[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float zs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int bin = i < v.n4 ? place(v.base + 4 * i + e, zs[e], key_of(zs[e])) : -1;
+        // the far end collects most elements when the temperature is low: one atomic a warp, and no mass there
+        const unsigned far = __ballot_sync(0xffffffffu, bin == kBins - 1);
+        if (far && lane == __ffs(far) - 1) atomicAdd(&s.h.count[kBins - 1], (uint32_t)__popc(far));
+        if (bin < 0) continue;
+        if (bin < kBins - 1) atomicAdd(&s.h.count[bin], 1u);
+        if (by_mass) {
+          int sh;
+          uint32_t W = weight31(zs[e], v.m, v.c, s.pow2, sh);
+          // relative to the bin's octave, which a weight is at most one below
+          W >>= min(sh - (level == 0 ? bin / kPerOctave : octave), 31);
+          if (W) {
+            atomicAdd(&s.h.hi[bin], W >> 16);
+            atomicAdd(&s.h.lo[bin], W & 0xFFFFu);
+          }
         }
-      }
-      // the far end collects most elements when the temperature is low: one atomic a warp
-      const unsigned far = __ballot_sync(0xffffffffu, bin == kBins - 1);
-      if (bin >= 0 && bin < kBins - 1) atomicAdd(&s.h.count[bin], 1u);
-      if (far && lane == __ffs(far) - 1) atomicAdd(&s.h.count[kBins - 1], (uint32_t)__popc(far));
-      if (w) {
-        atomicAdd(&s.h.hi[bin], (uint32_t)(w >> 16));
-        atomicAdd(&s.h.lo[bin], (uint32_t)(w & 0xFFFFu));
       }
     }
     cluster.sync();
@@ -257,9 +355,10 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         cnt += o->h.count[i];
         mass += ((uint64_t)o->h.hi[i] << 16) + o->h.lo[i];
       }
-      s0->mcount[i] = cnt;
-      s0->mmass[i] = (mass << (kUnit - 32)) >> (level == 0 ? i / kPerOctave : octave);
+      s0->all.count[i] = cnt;
+      s0->all.mass[i] = (mass << (kUnit - 30)) >> (level == 0 ? i / kPerOctave : octave);
     }
+    if (tid < 2) s.part_n[tid] = 0;
     cluster.sync();
     if (rank == 0) {
       constexpr int kPer = kBins / kSThreads;
@@ -267,11 +366,17 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       uint64_t mass[kPer], mb = 0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        cb += cnt[j] = s.mcount[tid * kPer + j];
-        mb += mass[j] = s.mmass[tid * kPer + j];
+        cb += cnt[j] = s.all.count[tid * kPer + j];
+        mb += mass[j] = s.all.mass[tid * kPer + j];
       }
-      if (tid == 0) s.cut_bin = -1, s.list_n = 0;
+      if (tid == 0) s.cut_bin = -1;
+      const uint64_t own = mb;
       block_scan(s, cb, mb);
+      if (by_mass && level == 0) {
+        if (tid == kSThreads - 1) s.cut_target = max(mul_frac(mb + own, v.p, true), (uint64_t)1);
+        __syncthreads();
+        target = s.cut_target;
+      }
       mb += before;
       int last = -1;  // the thread's last bin that counts
       uint64_t last_before = 0;
@@ -308,6 +413,7 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
     const int bin = s0->cut_bin;
     const uint32_t count = s0->cut_count;
     before = s0->cut_before;
+    if (by_mass) target = s0->cut_target;
     if (!by_mass) need = s0->cut_need;
     const bool one_key = level > 0 && shift == 0;
     if (level == 0) {
@@ -319,49 +425,79 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       low_key = top_key - low_key > span ? top_key - span : low_key;
     }
     if (count <= kList) {
-      // collect the bin's elements in the first CTA, rank them all against all
-      for (int i = tid; i < v.n; i += kSThreads) {
-        const float z = v.z[i];
-        const uint32_t key = key_of(z);
-        const int b = place(i, z, key);
-        if (level == 0 ? b != bin0 : b < 0) continue;
-        const uint32_t at = atomicAdd(&s0->list_n, 1u);
-        if (at < kList) {
-          s0->list.key[at] = key;
-          s0->list.idx[at] = v.base + i;
-          s0->list.w[at] = weight(z, v.m, v.c, s.pow2);
+      // list the bin's elements, and at level 0 those in front of it while they fit
+      for (int i0 = 0; i0 < v.n4; i0 += kSThreads) {
+        const int i = i0 + tid;
+        if (i >= v.n4) break;
+        const float4 q = v.z[i];
+        const float zs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t key = key_of(zs[e]), idx = v.base + 4 * i + e;
+          const int b = place(idx, zs[e], key);
+          if (b < 0 || (level == 0 && b > bin0)) continue;
+          const int sort = level == 0 && b < bin0;
+          if (sort && s.part_n[1] > kHalfList) continue;  // (a race that at most counts a few more)
+          const uint32_t at = atomicAdd(&s.part_n[sort], 1u);
+          if (at < kHalfList) s.part[sort][at] = Entry{weight(zs[e], v.m, v.c, s.pow2), key, idx};
         }
       }
       cluster.sync();
-      if (rank == 0) {
-        const int n = (int)min(s.list_n, (uint32_t)kList);
-        if (tid == 0) s.found = 0;
-        __syncthreads();
-        for (int pass = 0; pass < 2; ++pass) {
-          for (int e = tid; e < n; e += kSThreads) {
-            const uint32_t k = s.list.key[e], x = s.list.idx[e];
-            uint32_t rank_e = 0;
-            uint64_t front = before;
-            for (int j = 0; j < n; ++j) {
-              const uint32_t kj = s.list.key[j], xj = s.list.idx[j];
-              const bool ahead = kj > k || (kj == k && xj < x);
-              rank_e += ahead;
-              front += ahead ? s.list.w[j] : 0;
-            }
-            // the need-th; or the one whose weight takes the mass to the target (the last, should rounding leave none)
-            bool last = by_mass ? front < target && (target <= front + s.list.w[e] || rank_e == (uint32_t)n - 1) : rank_e == need - 1;
-            if (pass == 1) last = rank_e == 0;  // what lies in front reached the target by rounding: the bin's first
-            if (last) {
-              s.cut = Cut{k, x};
-              s.found = 1;
+      uint32_t n[2] = {0, 0}, most = 0;
+      for (int r = 0; r < C; ++r) {
+        const Shared* o = cluster.map_shared_rank(&s, r);
+        n[0] += o->part_n[0];
+        n[1] += o->part_n[1];
+        most = max(most, o->part_n[0]);
+      }
+      bool fits = level == 0 && n[0] + n[1] <= kList;
+      for (int r = 0; r < C; ++r) {
+        const Shared* o = cluster.map_shared_rank(&s, r);
+        fits &= o->part_n[1] <= kHalfList && o->part_n[0] <= kHalfList;
+      }
+      if (fits || most <= kHalfList) {
+        if (rank == 0) {
+          // gather the CTAs' lists
+          uint32_t to = 0;
+          for (int r = 0; r < C; ++r) {
+            const Shared* o = cluster.map_shared_rank(&s, r);
+            for (int sort = 0; sort < (fits ? 2 : 1); ++sort) {
+              const uint32_t len = o->part_n[sort];
+              for (uint32_t e = tid; e < len; e += kSThreads) s.list[to + e] = o->part[sort][e];
+              to += len;
             }
           }
+          if (tid == 0) s.found = 0;
           __syncthreads();
-          if (s.found) break;
+          if (fits) {
+            draw_from_list(s, v, (int)to, by_mass ? target : 0);
+          } else {
+            const int n_list = (int)to;
+            for (int pass = 0; pass < 2; ++pass) {
+              for (int e = tid; e < n_list; e += kSThreads) {
+                const Entry me = s.list[e];
+                uint32_t ahead = 0;
+                uint64_t front = before;
+                for (int j = 0; j < n_list; ++j) {
+                  const Entry o = s.list[j];
+                  if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) ++ahead, front += o.w;
+                }
+                // the need-th; or the one whose weight takes the mass to the target (the last, should rounding leave none)
+                bool last = by_mass ? front < target && (target <= front + me.w || ahead == to - 1) : ahead == need - 1;
+                if (pass == 1) last = ahead == 0;  // what lies in front reached the target by rounding: the bin's first
+                if (last) {
+                  s.cut = Cut{me.key, me.idx};
+                  s.found = 1;
+                }
+              }
+              __syncthreads();
+              if (s.found) break;
+            }
+          }
         }
+        cluster.sync();
+        return fits;
       }
-      cluster.sync();
-      return;
     }
     if (one_key) {
       // all `count` elements have the key top_key and one weight: the cut is the want-th of them in index order
@@ -371,10 +507,12 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         const uint64_t w = weight(logit_of(k), v.m, v.c, s.pow2), more = target > before ? target - before : 1;
         want = w ? (uint32_t)min((more + w - 1) / w, (uint64_t)count) : count;
       }
-      const int seg = (v.n + kSWarps - 1) / kSWarps, lo = min(warp * seg, v.n), hi = min(lo + seg, v.n);
-      auto equal = [&](int i) { return i < hi && key_of(v.z[i]) == k && (!limited || kept(k, v.base + i, limit)); };
+      const float* z = reinterpret_cast<const float*>(v.z);
+      const int n = 4 * v.n4, seg = (n + kSWarps - 1) / kSWarps, lo = min(warp * seg, n), hi = min(lo + seg, n);
+      auto equal = [&](int i) { return i < hi && key_of(z[i]) == k && (!limited || kept(k, v.base + i, limit)); };
       uint32_t mine = 0;
       for (int i0 = lo; i0 < hi; i0 += 32) mine += __popc(__ballot_sync(0xffffffffu, equal(i0 + lane)));
+      __syncthreads();
       if (lane == 0) s.wcnt[warp] = mine;
       __syncthreads();
       if (tid == 0) {
@@ -395,15 +533,19 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         }
       }
       cluster.sync();
-      return;
+      return false;
     }
     // the bin again, finer: first the keys it spans
     if (level == 0) {
       uint32_t hi = 0, lo = 0xFFFFFFFFu;
-      for (int i = tid; i < v.n; i += kSThreads) {
-        const float z = v.z[i];
-        const uint32_t key = key_of(z);
-        if (place(i, z, key) == bin0) hi = max(hi, key), lo = min(lo, key);
+      for (int i = tid; i < v.n4; i += kSThreads) {
+        const float4 q = v.z[i];
+        const float zs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t key = key_of(zs[e]);
+          if (place(v.base + 4 * i + e, zs[e], key) == bin0) hi = max(hi, key), lo = min(lo, key);
+        }
       }
       hi = __reduce_max_sync(0xffffffffu, hi);
       lo = __reduce_min_sync(0xffffffffu, lo);
@@ -425,7 +567,7 @@ __device__ void find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
     shift = 0;
     while (((top_key - low_key) >> shift) >= (uint32_t)(kBins - 1)) ++shift;  // the far bin stays free
     ++level;
-    cluster.sync();  // ccount, cfirst and the cut have been read
+    cluster.sync();  // ccount, cfirst, the lists' lengths and the cut have been read
   }
 }
 
@@ -478,7 +620,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     }
   }
   for (int i = head + vecs * kVec + tid; i < n; i += kSThreads) put(i, as_f32(src[i]));
-  for (int i = tid; i < 256; i += kSThreads) s.pow2[i] = make_float2(g_pow2.hi[i], g_pow2.lo[i]);
+  const int n4 = (n + 3) / 4;
+  if (tid < 4 * n4 - n) z[n + tid] = -INFINITY;
+  for (int i = tid; i < kTable; i += kSThreads) s.pow2[i] = g_pow2.v[i];
 
   const float T0 = a.temperature ? a.temperature[row] : 1.f;
   const int k0 = a.top_k ? a.top_k[row] : 0;
@@ -527,26 +671,30 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     m = 0.f;
     __syncthreads();
   }
-  const Slice v{z, n, base, m, rate_of(fminf(fmaxf(T0, 1e-30f), 1e30f))};
+  const bool top_k = k0 > 1 && k0 < a.vocab, top_p = p0 < 1.f;
+  const uint64_t least = q0 > 0.f ? (q0 >= 1.f ? 1ull << kUnit : mul_frac(1ull << kUnit, q0, true)) : 0;
+  const Slice v{reinterpret_cast<const float4*>(z), n4, base, m, rate_of(fminf(fmaxf(T0, 1e-30f), 1e30f)), top_k ? (uint32_t)k0 : 0,
+                top_p ? p0 : 1.f, least, u0 > 0.f ? fminf(u0, 0.99999994f) : 0.f, a.tokens + row, a.probs ? a.probs + row : nullptr};
 
   Cut cut{0, 0xFFFFFFFFu};
   bool limited = false;
-  if (k0 > 1 && k0 < a.vocab) {
-    find_cut(cluster, s, s0, v, cut, false, false, (uint32_t)k0, 0);
+  for (int step = 0; step < 2; ++step) {
+    if (step == 0 ? !top_k : !top_p) continue;
+    if (find_cut(cluster, s, s0, v, cut, limited, step == 1)) return;  // drawn
     cut = s0->cut;
     limited = true;
     cluster.sync();
   }
-  // each warp's contiguous share of the slice: its kept mass in wsum, the CTA's in ctotal
+  // each warp's contiguous share of the slice: its kept mass goes to wsum, the CTA's to ctotal
   const int seg = (n + kSWarps - 1) / kSWarps, lo = min(warp * seg, n), hi = min(lo + seg, n);
-  auto kept_weight = [&](int i, uint64_t least) -> uint64_t {
+  auto kept_weight = [&](int i) -> uint64_t {
     if (i >= hi || (limited && !kept(key_of(z[i]), base + i, cut))) return 0;
     const uint64_t w = weight(z[i], m, v.c, s.pow2);
     return w >= least ? w : 0;
   };
-  auto sum_kept = [&](uint64_t least) {
+  {
     uint64_t sum = 0;
-    for (int i = lo + lane; i < hi; i += 32) sum += kept_weight(i, least);
+    for (int i = lo + lane; i < hi; i += 32) sum += kept_weight(i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     __syncthreads();
@@ -558,19 +706,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
       s.ctotal = all;
     }
     cluster.sync();
-  };
-  if (p0 < 1.f) {
-    sum_kept(0);
-    uint64_t total = 0;
-    for (int r = 0; r < C; ++r) total += cluster.map_shared_rank(&s, r)->ctotal;
-    // front < total * p  <=>  front < ceil(total * p)
-    find_cut(cluster, s, s0, v, cut, limited, true, 0, max(mul_frac(total, p0, true), (uint64_t)1));
-    cut = s0->cut;
-    limited = true;
-    cluster.sync();
   }
-  const uint64_t least = q0 > 0.f ? (q0 >= 1.f ? 1ull << kUnit : mul_frac(1ull << kUnit, q0, true)) : 0;
-  sum_kept(least);
   uint64_t total = 0, front = 0;
   for (int r = 0; r < C; ++r) {
     const uint64_t t = cluster.map_shared_rank(&s, r)->ctotal;
@@ -579,10 +715,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   }
   for (int w = 0; w < warp; ++w) front += s.wsum[w];
   // sum > u * total  <=>  sum > floor(u * total)
-  const uint64_t at = mul_frac(total, u0 > 0.f ? fminf(u0, 0.99999994f) : 0.f, false);
+  const uint64_t at = mul_frac(total, v.u, false);
   if (front <= at && at < front + s.wsum[warp]) {
     for (int i0 = lo; i0 < hi && front <= at; i0 += 32) {
-      const uint64_t w = kept_weight(i0 + lane, least);
+      const uint64_t w = kept_weight(i0 + lane);
       uint64_t incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -591,7 +727,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
       }
       if (front + incl - w <= at && at < front + incl) {
         a.tokens[row] = (int32_t)(base + i0 + lane);
-        if (a.probs) a.probs[row] = (float)w / (float)total;
+        if (v.prob) *v.prob = (float)w / (float)total;
       }
       front += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -610,7 +746,7 @@ moe_status_t launch_sample(SampleArgs a, cudaStream_t st) {
   int C = 1;
   while (C < kMaxCluster && (a.vocab + C - 1) / C > 20480) C *= 2;
   while (C < kMaxCluster && (int64_t)a.rows * C * 2 <= sms && a.vocab / C > 4096) C *= 2;
-  a.slice = (((a.vocab + C - 1) / C) + 7) & ~7;
+  a.slice = (((a.vocab + C - 1) / C) + 7) & ~7;  // a multiple of the float4 and of 16 bytes of any type
   const int smem = (int)sizeof(Shared) + a.slice * 4;
   if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MOE_ERR_CUDA;

@@ -42,10 +42,6 @@ class Stats(C.Structure):
                 ("wait_ns", C.c_uint64), ("n_slots", C.c_int32), ("error", C.c_int32), ("rechecks", C.c_uint64)]
 
 
-class Heads(C.Structure):
-    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
-
-
 class NormRope(C.Structure):
     _fields_ = [("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("table", C.c_void_p), ("n_positions", C.c_int32),
                 ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("eps", C.c_float), ("weight_offset", C.c_float)]
@@ -95,16 +91,16 @@ def lib(build_if_missing=False):
         L.moe_destroy.argtypes = [p]
         L.moe_destroy.restype = None
         L.moe_route_noalloc.argtypes = [p, p, p, i32, i32, i32, i32, p, p, p]
-        heads, norm, cache, batch = (C.POINTER(x) for x in (Heads, NormRope, KvCacheDesc, KvBatchDesc))
+        # pointers to the structures of moe_model.h are passed as addresses
         L.moe_rope_table.argtypes = [i32, i32, C.c_double, p]
-        L.moe_qk_norm_rope.argtypes = [norm, i32, i32, i32, i32, heads, heads, i32, heads, heads, p, p]
+        L.moe_qk_norm_rope.argtypes = [p, i32, i32, i32, i32, p, p, i32, p, p, p, p]
         L.moe_kv_page_bytes.argtypes = [i32, i32, i32, i32]
         L.moe_kv_page_bytes.restype = C.c_size_t
-        L.moe_kv_append.argtypes = [cache, batch, i32, heads, heads, p]
-        L.moe_kv_append_norm_rope.argtypes = [cache, batch, norm, i32, i32, heads, heads, heads, heads, p, p]
-        L.moe_kv_read.argtypes = [cache, batch, i32, heads, heads, p]
-        L.moe_kv_attend_workspace.argtypes = [cache, batch, i32, i32, C.POINTER(C.c_size_t)]
-        L.moe_kv_attend.argtypes = [cache, batch, i32, i32, heads, heads, p, C.c_float, i32, p, C.c_size_t, p]
+        L.moe_kv_append.argtypes = [p, p, i32, p, p, p]
+        L.moe_kv_append_norm_rope.argtypes = [p, p, p, i32, i32, p, p, p, p, p, p]
+        L.moe_kv_read.argtypes = [p, p, i32, p, p, p]
+        L.moe_kv_attend_workspace.argtypes = [p, p, i32, i32, p]
+        L.moe_kv_attend.argtypes = [p, p, i32, i32, p, p, p, C.c_float, i32, p, C.c_size_t, p]
         L.moe_sample.argtypes = [p, i32, i32, i32, i64, p, p, p, p, p, p, p, p]
         L.moe_status_string.argtypes = [C.c_int]
         L.moe_status_string.restype = C.c_char_p

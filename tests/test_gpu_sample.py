@@ -44,7 +44,7 @@ def f32(v):
 
 
 def against(z, u, temperature, top_k, top_p, min_p):
-    """Equal tokens, except where u lies within 2^-28 of a border of the running sum (the sums are exact to about 2^-32 a
+    """Equal tokens, except where u lies within 2^-28 of a border of the running sum (the sums are exact to about 2^-31 a
     weight); probabilities to 2^-22 (a fp32 quotient of rounded operands)."""
     n = z.shape[0]
     tok, p = run(z, u, temperature, top_k, top_p, min_p)

@@ -49,20 +49,20 @@ def cache(moe, **kw):
     page = moe.lib().moe_kv_page_bytes(64, 2, 128, 8)
     d = dict(data=ADDR, data_bytes=10 * page, n_pages=10, page_size=64, n_kv_heads=2, head_dim=128, bits=8, status=ADDR)
     d.update(kw)
-    return moe.KvCacheDesc(**d)
+    return C.byref(moe.KvCacheDesc(**d))
 
 
 def batch(moe, **kw):
     d = dict(block_table=ADDR, seq_lens=ADDR, cu_tokens=ADDR, n_seqs=3, table_stride=4, max_pages=4, n_tokens=5,
              max_tokens=3)
     d.update(kw)
-    return moe.KvBatchDesc(**d)
+    return C.byref(moe.KvBatchDesc(**d))
 
 
 def heads(moe, dim=128, n=2, **kw):
     d = dict(data=ADDR, token_stride=n * dim, head_stride=dim)
     d.update(kw)
-    return moe.Heads(**d)
+    return C.byref((C.c_int64 * 3)(d["data"] or 0, d["token_stride"], d["head_stride"]))  # moe_heads_t
 
 
 BAD_CACHES = [dict(data=None), dict(data=ADDR + 8), dict(status=None), dict(status=ADDR + 2), dict(n_pages=0), dict(n_pages=11),
@@ -97,7 +97,7 @@ def test_append_and_read_refuse(moe):
 def norm(moe, **kw):
     d = dict(q_weight=ADDR, k_weight=ADDR, table=ADDR, n_positions=100, rot_dim=64, interleaved=0, eps=1e-6, weight_offset=0.0)
     d.update(kw)
-    return moe.NormRope(**d)
+    return C.byref(moe.NormRope(**d))
 
 
 def test_norm_rope_refuses(moe):
@@ -149,8 +149,9 @@ def test_attend_refuses(moe):
     assert call(dtype=2) == UNSUPPORTED and call(dtype=7) == INVALID
     assert call(b=batch(moe, n_tokens=1 << 24, max_tokens=1 << 24)) == UNSUPPORTED
     n = C.c_size_t(5)
+    ref = C.byref(n)
     assert L.moe_kv_attend_workspace(cache(moe), batch(moe), 4, 0, None) == INVALID
-    assert L.moe_kv_attend_workspace(cache(moe), batch(moe), 3, 0, n) == INVALID and n.value == 0
+    assert L.moe_kv_attend_workspace(cache(moe), batch(moe), 3, 0, ref) == INVALID and n.value == 0
 
 
 def test_sample_refuses(moe):
@@ -178,6 +179,7 @@ def test_binding_refuses_before_the_library(moe, monkeypatch):
         def __getattr__(self, name):
             raise AssertionError(name + " was called")
 
+    attention._native()  # the extension module holds the library's addresses; it declines all of what follows
     monkeypatch.setattr(moe, "lib", lambda: Library())
     z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)
     with pytest.raises(ValueError):  # host tensors
@@ -195,9 +197,13 @@ def test_binding_refuses_before_the_library(moe, monkeypatch):
     with pytest.raises(ValueError):
         sampling.sample(z(100), z(1, dt=torch.float32))
     c = attention.KvCache.__new__(attention.KvCache)
-    c.n_kv_heads, c.head_dim, c.device = 2, 128, torch.device("cpu")
+    c.n_kv_heads, c.head_dim, c.dev = 2, 128, -1
+    c.desc, c.data = moe.KvCacheDesc(n_kv_heads=2, head_dim=128), z(16, dt=torch.uint8)
+    c._at = C.addressof(c.desc)
     b = attention.KvBatch.__new__(attention.KvBatch)
-    b.n_tokens, b.device = 3, torch.device("cpu")
+    b.n_tokens, b.dev = 3, -1
+    b.desc = moe.KvBatchDesc(n_tokens=3)
+    b._at = C.addressof(b.desc)
     good = z(3, 2, 128)
     bad = [z(2, 2, 128), z(3, 4, 128), z(3, 2, 64), z(3, 2, 128, dt=torch.float16), z(3, 128, 2).transpose(1, 2), z(3, 2, 132)[..., 4:]]
     for x in bad:
