@@ -34,8 +34,8 @@ namespace {
 constexpr int kSThreads = 512, kSWarps = kSThreads / 32;
 constexpr int kBins = 1024, kPerOctave = 16;  // 64 octaves: beyond them a weight is 0 in units of 2^-45
 constexpr int kUnit = 45;                     // 2^18 weights of 2^45 fit 64 bits
-constexpr int kList = 768;                    // elements ranked against each other at most
-constexpr int kHalfList = kList / 2;          // what a CTA lists of either sort
+constexpr int kList = 512;                    // elements ranked against each other at most: one a thread
+constexpr int kHalfList = 384;                // what a CTA lists of either sort
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxCluster = 8;
 constexpr int kTable = 512;
@@ -106,8 +106,15 @@ __device__ __forceinline__ uint32_t weight31(float z, float m, const Rate& c, co
   s = (k >> 9) + 1;
   return (((__float_as_uint(t.x) & 0x7FFFFFu) | 0x800000u) << 7) + (uint32_t)(__float_as_int(low) - 0x4B400000);
 }
+// W 2^(15 - s) rounded to units of 2^-45, with 32-bit shifts and one wide multiply.
 __device__ __forceinline__ uint64_t to_units(uint32_t W, int s) {
-  return s >= 64 ? 0 : (((uint64_t)W << (kUnit - 30)) + ((1ull << s) >> 1)) >> s;
+  constexpr int kUp = kUnit - 30;
+  const uint32_t down = (uint32_t)max(s - kUp, 0);
+  const uint32_t mul = 1u << max(kUp - s, 0);
+  uint32_t half, w;
+  asm("shl.b32 %0, 1, %1;" : "=r"(half) : "r"(down));  // 0 from 32 on
+  asm("shr.u32 %0, %1, %2;" : "=r"(w) : "r"(W + (half >> 1)), "r"(down));
+  return (uint64_t)w * mul;
 }
 __device__ __forceinline__ uint64_t weight(float z, float m, const Rate& c, const float2* tab) {
   int s;
@@ -157,7 +164,7 @@ struct Entry {
   uint32_t key, idx;
 };
 
-struct Shared {
+struct alignas(16) Shared {
   // this CTA's histogram, and later its lists: elements of the cut's bin, and in front of it
   union {
     struct {
@@ -224,6 +231,8 @@ __device__ __forceinline__ uint64_t block_sum(Shared& s, uint64_t v) {
   return v;
 }
 
+static_assert(kSWarps == 2 * kMaxCluster, "a warp for each of the cluster's lists");
+
 // The slice of a row that a CTA holds, n4 float4 (the end filled with
 // -infinity), and what is asked of the row.
 struct Slice {
@@ -240,60 +249,83 @@ struct Slice {
   float* prob;
 };
 
+// Ranks the list's n <= kList elements against each other: place = how many
+// are ahead of this thread's element in the order, front = their mass.  With
+// few elements several neighbouring threads share one: thread t has element t / share of
+// n, and all of the sharers get its result.
+__device__ __forceinline__ void rank_list(const Shared& s, int n, int& share, uint32_t& place, uint64_t& front) {
+  share = 1;
+  while (share < 32 && n * share * 2 <= kSThreads) share *= 2;
+  const int e = threadIdx.x / share, part = threadIdx.x % share;
+  place = 0;
+  front = 0;
+  if (e < n) {
+    const Entry me = s.list[e];
+    const uint64_t rank = (uint64_t)me.key << 32 | ~me.idx;
+#pragma unroll 4
+    for (int i = part; i < n; i += share) {
+      const Entry o = s.list[i];
+      if (((uint64_t)o.key << 32 | ~o.idx) > rank) ++place, front += o.w;
+    }
+  }
+  for (int o = 1; o < share; o <<= 1) {
+    place += __shfl_xor_sync(0xffffffffu, place, o);
+    front += __shfl_xor_sync(0xffffffffu, front, o);
+  }
+}
+
 // The first CTA alone: every element that top-k and top-p can keep is in the
 // list, n of them; cut them, and draw the token.  target: the mass that top-p
 // asks for, or 0: its share of what top-k keeps of the list.
 __device__ void draw_from_list(Shared& s, const Slice& v, int n, uint64_t target) {
-  constexpr int kPer = (kList + kSThreads - 1) / kSThreads;
-  const int tid = threadIdx.x;
-  uint64_t front[kPer], w[kPer], sum = 0;
-  uint32_t place[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = tid + j * kSThreads;
-    front[j] = w[j] = 0;
-    place[j] = 0xFFFFFFFFu;
-    if (e < n) {
-      const Entry me = s.list[e];
-      uint32_t ahead = 0;
-      for (int i = 0; i < n; ++i) {
-        const Entry o = s.list[i];
-        if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) ++ahead, front[j] += o.w;
-      }
-      place[j] = ahead;
-      w[j] = v.k > 0 && ahead >= v.k ? 0 : me.w;
-      sum += w[j];
-    }
-  }
+  int share;
+  uint32_t place;
+  uint64_t front, w = 0;
+  rank_list(s, n, share, place, front);
+  const int e = threadIdx.x / share, part = threadIdx.x % share;
+  if (e < n && !(v.k > 0 && place >= v.k)) w = s.list[e].w;
   if (v.p < 1.f) {
     // front < sum * p  <=>  front < ceil(sum * p)
-    if (!target) target = max(mul_frac(block_sum(s, sum), v.p, true), (uint64_t)1);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (front[j] >= target) w[j] = 0;
+    if (!target) target = max(mul_frac(block_sum(s, part == 0 ? w : 0), v.p, true), (uint64_t)1);
+    if (front >= target) w = 0;
   }
-  sum = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (w[j] < v.least && place[j] != 0) w[j] = 0;
-    sum += w[j];
-  }
-  const uint64_t total = block_sum(s, sum);
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (tid + j * kSThreads < n) s.list[tid + j * kSThreads].w = w[j];
+  if (w < v.least && place != 0) w = 0;
+  const uint64_t total = block_sum(s, part == 0 ? w : 0);  // (its barriers: all have read the list)
+  if (e < n && part == 0) s.list[e].w = w;
   __syncthreads();
   // running sum > u * total  <=>  running sum > floor(u * total)
   const uint64_t at = mul_frac(total, v.u, false);
+  uint32_t idx = 0;
+  uint64_t below = 0;
+  if (e < n) {
+    idx = s.list[e].idx;
+#pragma unroll 4
+    for (int i = part; i < n; i += share) below += s.list[i].idx < idx ? s.list[i].w : 0;
+  }
+  for (int o = 1; o < share; o <<= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+  if (part == 0 && w != 0 && below <= at && at < below + w) {
+    *v.token = (int32_t)idx;
+    if (v.prob) *v.prob = (float)w / (float)total;
+  }
+}
+
+// Calls f(logit, index in the row) for the slice's elements, several loads of four in flight.
+template <typename F>
+__device__ __forceinline__ void each(const Slice& v, F f) {
+  constexpr int kAhead = 2;
+  for (int i0 = threadIdx.x; i0 < v.n4; i0 += kAhead * kSThreads) {
+    float4 q[kAhead];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (w[j] == 0) continue;
-    const uint32_t idx = s.list[tid + j * kSThreads].idx;
-    uint64_t below = 0;
-    for (int i = 0; i < n; ++i) below += s.list[i].idx < idx ? s.list[i].w : 0;
-    if (below <= at && at < below + w[j]) {
-      *v.token = (int32_t)idx;
-      if (v.prob) *v.prob = (float)w[j] / (float)total;
+    for (int j = 0; j < kAhead; ++j)
+      q[j] = i0 + j * kSThreads < v.n4 ? v.z[i0 + j * kSThreads] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j * kSThreads;
+      if (j > 0 && i >= v.n4) break;
+      f(q[j].x, v.base + 4 * i);
+      f(q[j].y, v.base + 4 * i + 1);
+      f(q[j].z, v.base + 4 * i + 2);
+      f(q[j].w, v.base + 4 * i + 3);
     }
   }
 }
@@ -312,7 +344,8 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
   uint32_t need = v.k;
   uint64_t before = 0, target = 0;  // mass in front of the range; the mass to reach (set at level 0)
   // is an element among those looked at, and in which bin
-  auto place = [&](uint32_t idx, float z, uint32_t key) -> int {
+  auto place = [&](uint32_t idx, float z) -> int {
+    const uint32_t key = key_of(z);
     if (limited && !kept(key, idx, limit)) return -1;
     const int b0 = bin_of(y_of(z, v.m, v.c));
     if (level == 0) return b0;
@@ -321,30 +354,29 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
   for (;;) {
     for (int i = tid; i < kBins; i += kSThreads) s.h.count[i] = s.h.hi[i] = s.h.lo[i] = 0;
     __syncthreads();
-    for (int i0 = 0; i0 < v.n4; i0 += kSThreads) {
-      const int i = i0 + tid;
-      const float4 q = i < v.n4 ? v.z[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float zs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int bin = i < v.n4 ? place(v.base + 4 * i + e, zs[e], key_of(zs[e])) : -1;
-        // the far end collects most elements when the temperature is low: one atomic a warp, and no mass there
-        const unsigned far = __ballot_sync(0xffffffffu, bin == kBins - 1);
-        if (far && lane == __ffs(far) - 1) atomicAdd(&s.h.count[kBins - 1], (uint32_t)__popc(far));
-        if (bin < 0) continue;
-        if (bin < kBins - 1) atomicAdd(&s.h.count[bin], 1u);
-        if (by_mass) {
-          int sh;
-          uint32_t W = weight31(zs[e], v.m, v.c, s.pow2, sh);
-          // relative to the bin's octave, which a weight is at most one below
-          W >>= min(sh - (level == 0 ? bin / kPerOctave : octave), 31);
-          if (W) {
-            atomicAdd(&s.h.hi[bin], W >> 16);
-            atomicAdd(&s.h.lo[bin], W & 0xFFFFu);
-          }
+    uint32_t far = 0;  // the last bin collects most elements when the temperature is low: counted apart (their mass is 0)
+    each(v, [&](float z, uint32_t idx) {
+      const int bin = place(idx, z);
+      if (bin < 0) return;
+      if (bin == kBins - 1) {
+        ++far;
+        if (!by_mass) return;
+      } else {
+        atomicAdd(&s.h.count[bin], 1u);
+      }
+      if (by_mass) {
+        int sh;
+        uint32_t W = weight31(z, v.m, v.c, s.pow2, sh);
+        // relative to the bin's octave, which a weight is at most one below
+        W >>= min(sh - (level == 0 ? bin / kPerOctave : octave), 31);
+        if (W) {
+          atomicAdd(&s.h.hi[bin], W >> 16);
+          atomicAdd(&s.h.lo[bin], W & 0xFFFFu);
         }
       }
-    }
+    });
+    far = __reduce_add_sync(0xffffffffu, far);
+    if (lane == 0 && far) atomicAdd(&s.h.count[kBins - 1], far);
     cluster.sync();
     // every CTA adds up its share of the bins over the cluster, for the first one
     for (int i = rank * (kBins / C) + tid; i < (rank + 1) * (kBins / C); i += kSThreads) {
@@ -426,73 +458,66 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
     }
     if (count <= kList) {
       // list the bin's elements, and at level 0 those in front of it while they fit
-      for (int i0 = 0; i0 < v.n4; i0 += kSThreads) {
-        const int i = i0 + tid;
-        if (i >= v.n4) break;
-        const float4 q = v.z[i];
-        const float zs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t key = key_of(zs[e]), idx = v.base + 4 * i + e;
-          const int b = place(idx, zs[e], key);
-          if (b < 0 || (level == 0 && b > bin0)) continue;
-          const int sort = level == 0 && b < bin0;
-          if (sort && s.part_n[1] > kHalfList) continue;  // (a race that at most counts a few more)
-          const uint32_t at = atomicAdd(&s.part_n[sort], 1u);
-          if (at < kHalfList) s.part[sort][at] = Entry{weight(zs[e], v.m, v.c, s.pow2), key, idx};
-        }
-      }
+      const float y_end = bin0 == kBins - 1 ? INFINITY : (float)(bin0 + 1) / kPerOctave;
+      each(v, [&](float z, uint32_t idx) {
+        if (!((v.m - z) * v.c.h <= y_end)) return;  // (most elements lie behind the bin)
+        const int b = place(idx, z);
+        if (b < 0 || (level == 0 && b > bin0)) return;
+        const int sort = level == 0 && b < bin0;
+        if (sort && s.part_n[1] > kHalfList) return;  // (a race that at most counts a few more)
+        const uint32_t at = atomicAdd(&s.part_n[sort], 1u);
+        if (at < kHalfList) s.part[sort][at] = Entry{weight(z, v.m, v.c, s.pow2), key_of(z), idx};
+      });
       cluster.sync();
-      uint32_t n[2] = {0, 0}, most = 0;
-      for (int r = 0; r < C; ++r) {
-        const Shared* o = cluster.map_shared_rank(&s, r);
-        n[0] += o->part_n[0];
-        n[1] += o->part_n[1];
-        most = max(most, o->part_n[0]);
+      uint32_t n0 = 0, n1 = 0;
+      if (lane < C) {
+        const Shared* o = cluster.map_shared_rank(&s, lane);
+        n0 = o->part_n[0];
+        n1 = o->part_n[1];
       }
-      bool fits = level == 0 && n[0] + n[1] <= kList;
-      for (int r = 0; r < C; ++r) {
-        const Shared* o = cluster.map_shared_rank(&s, r);
-        fits &= o->part_n[1] <= kHalfList && o->part_n[0] <= kHalfList;
-      }
-      if (fits || most <= kHalfList) {
+      const bool whole0 = __all_sync(0xffffffffu, n0 <= kHalfList), whole1 = __all_sync(0xffffffffu, n1 <= kHalfList);
+      const bool fits = level == 0 && whole0 && whole1 && __reduce_add_sync(0xffffffffu, n0 + n1) <= kList;
+      if (whole0) {
         if (rank == 0) {
-          // gather the CTAs' lists
-          uint32_t to = 0;
-          for (int r = 0; r < C; ++r) {
+          // gather the CTAs' lists: one warp a list
+          uint32_t mine = fits ? n0 + n1 : n0, start = mine;
+#pragma unroll
+          for (int o = 1; o < kMaxCluster; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, start, o);
+            if (lane >= o) start += x;
+          }
+          const int to = (int)__shfl_sync(0xffffffffu, start, kMaxCluster - 1);
+          start -= mine;
+          const int r = warp >> 1, sort = warp & 1;  // kSWarps = 2 kMaxCluster
+          const uint32_t at = __shfl_sync(0xffffffffu, start, r) + (sort ? __shfl_sync(0xffffffffu, n0, r) : 0);
+          const uint32_t len0 = __shfl_sync(0xffffffffu, n0, r), len1 = __shfl_sync(0xffffffffu, n1, r);
+          const uint32_t len = sort ? (fits ? len1 : 0) : len0;
+          if (r < C) {
             const Shared* o = cluster.map_shared_rank(&s, r);
-            for (int sort = 0; sort < (fits ? 2 : 1); ++sort) {
-              const uint32_t len = o->part_n[sort];
-              for (uint32_t e = tid; e < len; e += kSThreads) s.list[to + e] = o->part[sort][e];
-              to += len;
-            }
+            for (uint32_t e = lane; e < len; e += 32) s.list[at + e] = o->part[sort][e];
           }
           if (tid == 0) s.found = 0;
           __syncthreads();
           if (fits) {
-            draw_from_list(s, v, (int)to, by_mass ? target : 0);
+            draw_from_list(s, v, to, by_mass ? target : 0);
           } else {
-            const int n_list = (int)to;
-            for (int pass = 0; pass < 2; ++pass) {
-              for (int e = tid; e < n_list; e += kSThreads) {
-                const Entry me = s.list[e];
-                uint32_t ahead = 0;
-                uint64_t front = before;
-                for (int j = 0; j < n_list; ++j) {
-                  const Entry o = s.list[j];
-                  if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) ++ahead, front += o.w;
-                }
-                // the need-th; or the one whose weight takes the mass to the target (the last, should rounding leave none)
-                bool last = by_mass ? front < target && (target <= front + me.w || ahead == to - 1) : ahead == need - 1;
-                if (pass == 1) last = ahead == 0;  // what lies in front reached the target by rounding: the bin's first
-                if (last) {
-                  s.cut = Cut{me.key, me.idx};
-                  s.found = 1;
-                }
+            int share;
+            uint32_t ahead;
+            uint64_t front;
+            rank_list(s, to, share, ahead, front);
+            front += before;
+            const int e = tid / share;
+            if (e < to) {
+              const Entry me = s.list[e];
+              // the need-th; or the one whose weight takes the mass to the target (the last, should rounding leave none)
+              if (by_mass ? front < target && (target <= front + me.w || ahead == (uint32_t)to - 1) : ahead == need - 1) {
+                s.cut = Cut{me.key, me.idx};
+                s.found = 1;
               }
-              __syncthreads();
-              if (s.found) break;
             }
+            __syncthreads();
+            // what lies in front of the bin may have reached the target by rounding: then its first element is the cut
+            if (!s.found && e < to && ahead == 0) s.cut = Cut{s.list[e].key, s.list[e].idx};
           }
         }
         cluster.sync();
@@ -538,15 +563,9 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
     // the bin again, finer: first the keys it spans
     if (level == 0) {
       uint32_t hi = 0, lo = 0xFFFFFFFFu;
-      for (int i = tid; i < v.n4; i += kSThreads) {
-        const float4 q = v.z[i];
-        const float zs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t key = key_of(zs[e]);
-          if (place(v.base + 4 * i + e, zs[e], key) == bin0) hi = max(hi, key), lo = min(lo, key);
-        }
-      }
+      each(v, [&](float z, uint32_t idx) {
+        if (place(idx, z) == bin0) hi = max(hi, key_of(z)), lo = min(lo, key_of(z));
+      });
       hi = __reduce_max_sync(0xffffffffu, hi);
       lo = __reduce_min_sync(0xffffffffu, lo);
       if (tid == 0) s.cfirst = 0xFFFFFFFFu, s.ccount = 0;
@@ -640,8 +659,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     s.cfirst = 0xFFFFFFFFu;
   }
   cluster.sync();
-  float m = -INFINITY;
-  for (int r = 0; r < C; ++r) m = fmaxf(m, cluster.map_shared_rank(&s, r)->cmax);
+  float m = lane < C ? cluster.map_shared_rank(&s, lane)->cmax : -INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 
   if (m == -INFINITY) {
     if (rank == 0 && tid == 0) {
@@ -685,16 +705,25 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     limited = true;
     cluster.sync();
   }
-  // each warp's contiguous share of the slice: its kept mass goes to wsum, the CTA's to ctotal
-  const int seg = (n + kSWarps - 1) / kSWarps, lo = min(warp * seg, n), hi = min(lo + seg, n);
-  auto kept_weight = [&](int i) -> uint64_t {
-    if (i >= hi || (limited && !kept(key_of(z[i]), base + i, cut))) return 0;
-    const uint64_t w = weight(z[i], m, v.c, s.pow2);
+  // each warp's contiguous share of the slice, four neighbours a lane: its kept mass goes to wsum, the CTA's to ctotal
+  const int seg = (n4 + kSWarps - 1) / kSWarps, lo = min(warp * seg, n4), hi = min(lo + seg, n4);
+  const float z_cut = limited ? logit_of(cut.key) : -INFINITY;
+  auto kept_weight = [&](float zi, uint32_t idx) -> uint64_t {
+    if (zi < z_cut || (limited && !kept(key_of(zi), idx, cut))) return 0;
+    const uint64_t w = weight(zi, m, v.c, s.pow2);
     return w >= least ? w : 0;
   };
+  auto load4 = [&](int i) { return i < hi ? v.z[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); };
   {
     uint64_t sum = 0;
-    for (int i = lo + lane; i < hi; i += 32) sum += kept_weight(i);
+    for (int i0 = lo + lane; i0 < hi; i0 += 64) {
+      const float4 q[2] = {load4(i0), load4(i0 + 32)};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t idx = base + 4 * (i0 + 32 * j);
+        sum += kept_weight(q[j].x, idx) + kept_weight(q[j].y, idx + 1) + kept_weight(q[j].z, idx + 2) + kept_weight(q[j].w, idx + 3);
+      }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     __syncthreads();
@@ -707,27 +736,37 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     }
     cluster.sync();
   }
-  uint64_t total = 0, front = 0;
-  for (int r = 0; r < C; ++r) {
-    const uint64_t t = cluster.map_shared_rank(&s, r)->ctotal;
-    if (r < rank) front += t;
-    total += t;
+  uint64_t part = lane < C ? cluster.map_shared_rank(&s, lane)->ctotal : 0, total = part, front = lane < rank ? part : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    front += __shfl_xor_sync(0xffffffffu, front, o);
   }
   for (int w = 0; w < warp; ++w) front += s.wsum[w];
   // sum > u * total  <=>  sum > floor(u * total)
   const uint64_t at = mul_frac(total, v.u, false);
   if (front <= at && at < front + s.wsum[warp]) {
     for (int i0 = lo; i0 < hi && front <= at; i0 += 32) {
-      const uint64_t w = kept_weight(i0 + lane);
-      uint64_t incl = w;
+      const float4 q = load4(i0 + lane);
+      const float zs[4] = {q.x, q.y, q.z, q.w};
+      const uint32_t idx = base + 4 * (i0 + lane);
+      uint64_t w[4], incl = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) incl += w[e] = kept_weight(zs[e], idx + e);
+      const uint64_t four = incl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
       }
-      if (front + incl - w <= at && at < front + incl) {
-        a.tokens[row] = (int32_t)(base + i0 + lane);
-        if (v.prob) *v.prob = (float)w / (float)total;
+      uint64_t below = front + incl - four;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (below <= at && at < below + w[e]) {
+          *v.token = (int32_t)(idx + e);
+          if (v.prob) *v.prob = (float)w[e] / (float)total;
+        }
+        below += w[e];
       }
       front += __shfl_sync(0xffffffffu, incl, 31);
     }
