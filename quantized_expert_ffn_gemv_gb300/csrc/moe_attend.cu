@@ -102,7 +102,7 @@ __device__ __forceinline__ int out_dim(int j, int c) {
 template <int D, int BITS, int NT>
 struct RowsPlan {
   static constexpr int kHalf = kv_half_bytes(D, BITS);
-  static constexpr int kBlocks = D * NT >= 512 || (D == 256 && BITS == 8) ? 2 : 3;
+  static constexpr int kBlocks = NT == 4 || D * NT >= 512 || (D == 256 && BITS == 8) ? 2 : 3;
   static constexpr int kRingBytes = kBlocks == 2 ? 26112 : D == 256 ? 18432 : 17408;
   static constexpr int kEntries = (kRingBytes / kHalf) < 12 ? (kRingBytes / kHalf) : 12;
   static constexpr int kRing = kEntries * kHalf;          // bytes a warp
@@ -114,28 +114,37 @@ struct RowsPlan {
   static_assert(kEntries >= 3, "a ring of three halves at least");
 };
 
+// (v & mask) | bits in one instruction; `bits` has to be a register (see kernel).
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "n"(MASK), "r"(bits));
+  return r;
+}
+
 // Eight stored integers of a key as the fp16 operand pairs of two k16 steps.
+// magic: 0x6400 in both halves, the fp16 exponent at which a mantissa step is 1.
 template <int BITS>
-__device__ __forceinline__ void key_operands(uint32_t (&k)[4], uint32_t at) {
+__device__ __forceinline__ void key_operands(uint32_t (&k)[4], uint32_t at, uint32_t magic) {
   if (BITS == 8) {
     const uint2 w = lds64(at);
-    k[0] = hsub2(prmt(w.x, 0x64646464u, 0x4140), 0x64806480u);
-    k[1] = hsub2(prmt(w.x, 0x64646464u, 0x4342), 0x64806480u);
-    k[2] = hsub2(prmt(w.y, 0x64646464u, 0x4140), 0x64806480u);
-    k[3] = hsub2(prmt(w.y, 0x64646464u, 0x4342), 0x64806480u);
+    k[0] = hsub2(prmt(w.x, magic, 0x5150), 0x64806480u);
+    k[1] = hsub2(prmt(w.x, magic, 0x5352), 0x64806480u);
+    k[2] = hsub2(prmt(w.y, magic, 0x5150), 0x64806480u);
+    k[3] = hsub2(prmt(w.y, magic, 0x5352), 0x64806480u);
   } else {
     const uint32_t w = lds32(at), w8 = w >> 8;
-    k[0] = hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-    k[1] = hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
-    k[2] = hsub2((w8 & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-    k[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+    k[0] = hsub2(and_or<0x000F000Fu>(w, magic), 0x64086408u);
+    k[1] = hfma2(and_or<0x00F000F0u>(w, magic), 0x2C002C00u, 0xD480D480u);
+    k[2] = hsub2(and_or<0x000F000Fu>(w8, magic), 0x64086408u);
+    k[3] = hfma2(and_or<0x00F000F0u>(w8, magic), 0x2C002C00u, 0xD480D480u);
   }
 }
 
 // One warp's products of a 32-key tile: s[i][n] holds keys 16 i + g and
 // 16 i + 8 + g (g = lane / 4) against rows 8 n + 2 t and + 1 (t = lane % 4).
 template <int D, int BITS, int NT>
-__device__ __forceinline__ void score_tile(float (&s)[2][NT][4], uint32_t kb, uint32_t qf, int lane) {
+__device__ __forceinline__ void score_tile(float (&s)[2][NT][4], uint32_t kb, uint32_t qf, int lane, uint32_t magic) {
   constexpr int R = kv_row_bytes(D, BITS), NC = R / 16;
   const int g = lane >> 2, t = lane & 3, turn = kv_turn(g) & (NC - 1);
 #pragma unroll
@@ -147,8 +156,8 @@ __device__ __forceinline__ void score_tile(float (&s)[2][NT][4], uint32_t kb, ui
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t k0[4], k1[4];
-      key_operands<BITS>(k0, kb + (16 * i + g) * R + at);
-      key_operands<BITS>(k1, kb + (16 * i + 8 + g) * R + at);
+      key_operands<BITS>(k0, kb + (16 * i + g) * R + at, magic);
+      key_operands<BITS>(k1, kb + (16 * i + 8 + g) * R + at, magic);
       const uint32_t sc = kb + kKvTile * R + (b * kKvTile + 16 * i + g) * 2;
       const float d0 = __half2float(__ushort_as_half((uint16_t)lds16(sc)));
       const float d1 = __half2float(__ushort_as_half((uint16_t)lds16(sc + 16)));
@@ -171,7 +180,7 @@ __device__ __forceinline__ void score_tile(float (&s)[2][NT][4], uint32_t kb, ui
 // do non-finite scales (the caller deals with the rows that see them).
 template <int D, int BITS, int NT>
 __device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint32_t (&p)[NT][2], uint32_t vb, int u, int lane,
-                                           bool edge, int lim) {
+                                           bool edge, int lim, uint32_t magic) {
   constexpr int R = kv_row_bytes(D, BITS), NC = R / 16, RUN = D / 8;
   constexpr int kRuns = (BITS == 8 && D == 256) ? 2 : 1;  // runs of RUN / kRuns elements a lane group has
   constexpr int kWords = RUN / kRuns * BITS / 32;         // 32-bit words of a run: 1, 2 or 4
@@ -214,10 +223,10 @@ __device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint
         for (int h = 0; h < 2; ++h) {
           const uint32_t x = prmt(v[0][w], v[1][w], h ? 0x7362 : 0x5140), y = prmt(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
           uint32_t a[4];
-          a[0] = hmul2(hsub2(prmt(x, 0x64646464u, 0x4140), 0x64806480u), sc[0]);
-          a[1] = hmul2(hsub2(prmt(x, 0x64646464u, 0x4342), 0x64806480u), sc[0]);
-          a[2] = hmul2(hsub2(prmt(y, 0x64646464u, 0x4140), 0x64806480u), sc[1]);
-          a[3] = hmul2(hsub2(prmt(y, 0x64646464u, 0x4342), 0x64806480u), sc[1]);
+          a[0] = hmul2(hsub2(prmt(x, magic, 0x5150), 0x64806480u), sc[0]);
+          a[1] = hmul2(hsub2(prmt(x, magic, 0x5352), 0x64806480u), sc[0]);
+          a[2] = hmul2(hsub2(prmt(y, magic, 0x5150), 0x64806480u), sc[1]);
+          a[3] = hmul2(hsub2(prmt(y, magic, 0x5352), 0x64806480u), sc[1]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma_f16(o[r * 8 + 2 * w + h][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
         }
@@ -228,10 +237,10 @@ __device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t a[4];
-            a[0] = hmul2(hsub2((x & 0x000F000Fu) | 0x64006400u, 0x64086408u), sc[0]);
-            a[1] = hmul2(hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), sc[0]);
-            a[2] = hmul2(hsub2((y & 0x000F000Fu) | 0x64006400u, 0x64086408u), sc[1]);
-            a[3] = hmul2(hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), sc[1]);
+            a[0] = hmul2(hsub2(and_or<0x000F000Fu>(x, magic), 0x64086408u), sc[0]);
+            a[1] = hmul2(hfma2(and_or<0x00F000F0u>(x, magic), 0x2C002C00u, 0xD480D480u), sc[0]);
+            a[2] = hmul2(hsub2(and_or<0x000F000Fu>(y, magic), 0x64086408u), sc[1]);
+            a[3] = hmul2(hfma2(and_or<0x00F000F0u>(y, magic), 0x2C002C00u, 0xD480D480u), sc[1]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_f16(o[4 * w + 2 * q + h][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
             x >>= 8, y >>= 8;
@@ -303,8 +312,13 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
 
   int b = s_b;
   long long base = s_base, cur = w0;
-  unsigned issued = 0, used = 0;  // halves over the life of the warp's ring
+  int in_slot = 0, out_slot = 0;  // the ring's next entry to fill and to use
+  uint32_t phase = 0;             // of the entry to use
   bool timed_out = false;
+  // the exponent of the dequantisation in a register the compiler cannot see through: with two constants an
+  // and-or would take two instructions
+  uint32_t magic = 0x64006400u;
+  asm volatile("" : "+r"(magic));
   const int g = lane >> 2, tq = lane & 3;
   while (cur < w1) {
     const Seq sq = seq_at(a, t, b);
@@ -325,50 +339,50 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
     const int rows = min(kRows, sq.n * t.group - rt * kRows);
 
     __syncthreads();  // the previous piece's merge has been read
-    if (lane == 0) fence_async_shared();
-    __syncwarp();
-    // this warp's tiles t0 + warp, + 4, ...; lane j holds the page of the (first + j)-th
+    fence_async_shared();
+    // this warp's tiles t0 + warp, + 4, ...; lane j holds the address of the (first + j)-th, and issues its copies
     const int nt = (t1 - t0 - warp + kAttWarps - 1) / kAttWarps;
-    int first = 0, pages = -1;
+    int first = 0;
+    const uint8_t* mine_src = nullptr;
     bool bad_page = false;
     auto load_pages = [&](int from) {
       first = from;
       const int i = from + lane;
-      pages = 0;
       if (i < nt) {
-        const int pi = kv_page_of(a, (t0 + warp + kAttWarps * i) * kKvTile);
-        pages = pi < a.max_pages ? __ldg(a.table + (size_t)b * a.table_stride + pi) : -1;
-        if ((unsigned)pages >= (unsigned)a.n_pages) {
+        const int pos = (t0 + warp + kAttWarps * i) * kKvTile, pi = kv_page_of(a, pos);
+        int page = pi < a.max_pages ? __ldg(a.table + (size_t)b * a.table_stride + pi) : -1;
+        if ((unsigned)page >= (unsigned)a.n_pages) {
           if (sq.len > 0) bad_page = true;  // an empty sequence's one tile holds nothing that is seen
-          pages = 0;                        // in bounds; the rows become NaN
+          page = 0;                         // in bounds; the rows become NaN
         }
+        mine_src = a.data + (size_t)page * a.page_bytes + (size_t)head * a.head_bytes +
+                   (size_t)((pos - pi * a.page_size) / kKvTile) * (2 * P::kHalf);
       }
     };
-    const uint8_t* head_data = a.data + (size_t)head * a.head_bytes;
     int sent = 0;  // halves of this piece issued
     auto issue = [&]() {
+      if (sent >= 2 * nt) return;
       const int i = sent >> 1;
-      if (i >= nt) return;
       if (i >= first + 32) load_pages(i);
-      const int page = __shfl_sync(0xffffffffu, pages, i - first);
-      if (lane == 0) {
-        const int pos = (t0 + warp + kAttWarps * i) * kKvTile;
-        const int in_page = pos - kv_page_of(a, pos) * a.page_size;
-        const uint8_t* src = head_data + (size_t)page * a.page_bytes + (size_t)(in_page / kKvTile) * (2 * P::kHalf) +
-                             (sent & 1) * P::kHalf;
-        const unsigned slot = issued % P::kEntries;
-        mbar_expect_tx(bars + slot * 8, P::kHalf);
-        bulk_g2s(ring + slot * P::kHalf, src, P::kHalf, bars + slot * 8);
+      if (lane == i - first) {
+        mbar_expect_tx(bars + in_slot * 8, P::kHalf);
+        bulk_g2s(ring + in_slot * P::kHalf, mine_src + (sent & 1) * P::kHalf, P::kHalf, bars + in_slot * 8);
       }
-      ++issued;
+      in_slot = in_slot + 1 == P::kEntries ? 0 : in_slot + 1;
       ++sent;
+    };
+    // Gives the slot just read back to the producer and moves on.
+    auto release = [&]() {
+      if (++out_slot == P::kEntries) out_slot = 0, phase ^= 1;
+      __syncwarp();
+      issue();
     };
     load_pages(0);
     for (int e = 0; e < P::kEntries; ++e) issue();
 
     // Queries: D / 8 threads a row, 8 elements each, in the order of the
     // operand pairs.  The row's largest magnitude sets the power of two it is
-    // divided by; a negative scale goes into the sign.
+    // divided by; a negative scale goes into the sign (and 0 into the query), so that the scores' factor is positive.
     {
       constexpr int TPR = D / 8;
 #pragma unroll
@@ -393,6 +407,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         e = big > 0.f && e < 128 ? min(max(e, -120), 120) : 0;
         float down = __uint_as_float((uint32_t)(127 - e) << 23);
         if (t.scale_log2 < 0.f) down = -down;
+        if (t.scale_log2 == 0.f) down = 0.f;
         if (row < kRows) {
           if (d8 == 0) row_exp[row] = __uint_as_float((uint32_t)(127 + e) << 23);
           uint32_t h[4];
@@ -414,7 +429,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         const int row = 8 * n + 2 * tq + h;
         m[n][h] = -INFINITY;
         l[n][h] = 0.f;
-        c[n][h] = fabsf(t.scale_log2) * row_exp[row];
+        c[n][h] = t.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(t.scale_log2) * row_exp[row], FLT_MIN);
         see[n][h] = row < rows ? sq.len - sq.n + (rt * kRows + row) / t.group : -1;
       }
 #pragma unroll
@@ -431,12 +446,9 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
       const bool edge = key0 + kKvTile - 1 > see_min;
       float s[2][NT][4];
       {
-        const unsigned slot = used % P::kEntries;
-        if (!mbar_wait(bars + slot * 8, (used / P::kEntries) & 1)) timed_out = true;
-        score_tile<D, BITS, NT>(s, ring + slot * P::kHalf, qf, lane);
-        ++used;
-        __syncwarp();
-        issue();
+        if (!mbar_wait(bars + out_slot * 8, phase)) timed_out = true;
+        score_tile<D, BITS, NT>(s, ring + out_slot * P::kHalf, qf, lane, magic);
+        release();
       }
       if (edge) {
 #pragma unroll
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
             if (key + 8 > see[n][1]) s[x][n][3] = -INFINITY;
           }
       }
-      // maxima in units of log2 (c >= 0, so the largest product has the largest score)
+      // maxima in units of log2 (c > 0, so the largest product has the largest score)
       float top[NT][2];
       bool grew = false;
 #pragma unroll
@@ -460,7 +472,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
           float v = fmaxf(fmaxf(s[0][n][h], s[0][n][h + 2]), fmaxf(s[1][n][h], s[1][n][h + 2]));
 #pragma unroll
           for (int of = 4; of < 32; of <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, of));
-          top[n][h] = v == -INFINITY ? v : v * c[n][h];
+          top[n][h] = v * c[n][h];
           grew |= top[n][h] > m[n][h];
         }
       if (__any_sync(0xffffffffu, grew)) {
@@ -488,7 +500,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         for (int x = 0; x < 2; ++x) {
           float e[4];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) e[h] = ex2(edge && s[x][n][h] == -INFINITY ? -INFINITY : fmaf(s[x][n][h], c[n][h & 1], h & 1 ? z1 : z0));
+          for (int h = 0; h < 4; ++h) e[h] = ex2(fmaf(s[x][n][h], c[n][h & 1], h & 1 ? z1 : z0));
           l[n][0] += e[0] + e[2];
           l[n][1] += e[1] + e[3];
           p[x][n][0] = transpose8(pack2<false>(e[0], e[1]));
@@ -496,12 +508,11 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         }
       }
       {
-        const unsigned slot = used % P::kEntries;
-        if (!mbar_wait(bars + slot * 8, (used / P::kEntries) & 1)) timed_out = true;
-        const uint32_t vb = ring + slot * P::kHalf;
+        if (!mbar_wait(bars + out_slot * 8, phase)) timed_out = true;
+        const uint32_t vb = ring + out_slot * P::kHalf;
         const int lim = see_max + 1 - key0;
-        value_step<D, BITS, NT>(o, p[0], vb, 0, lane, edge, lim);
-        value_step<D, BITS, NT>(o, p[1], vb, 1, lane, edge, lim);
+        value_step<D, BITS, NT>(o, p[0], vb, 0, lane, edge, lim, magic);
+        value_step<D, BITS, NT>(o, p[1], vb, 1, lane, edge, lim, magic);
         if (edge) {
           // value_step took non-finite scales for 0, so that rows that do not see such a key stay clean; the rows that do become NaN
           bool odd = false;
@@ -517,9 +528,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
                 if (key <= see[n][h]) l[n][h] = __uint_as_float(kNaN);
           }
         }
-        ++used;
-        __syncwarp();
-        issue();
+        release();
       }
     }
     bool spoiled = false;
@@ -741,7 +750,7 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   int sms = 0;
   st = device_sms(&sms);
   if (st != MOE_OK) return st;
-  p->parts = sms * (cache->head_dim * p->tile_rows >= 4096 || (cache->head_dim == 256 && cache->bits == 8) ? 2 : 3);
+  p->parts = sms * (p->tile_rows == 32 || cache->head_dim * p->tile_rows >= 4096 || (cache->head_dim == 256 && cache->bits == 8) ? 2 : 3);
   p->ws = plan_workspace(p->parts, p->tile_rows, cache->head_dim, p->segments);
   return MOE_OK;
 }
