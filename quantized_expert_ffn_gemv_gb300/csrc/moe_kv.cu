@@ -95,11 +95,20 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint16_t& scale)
   scale = __half_as_ushort(__float2half_rn(__uint_as_float(m) / top));
   if (m > 0x477E0000u) scale = 0x7FFFu;  // above 65024 (NaN and infinity among them): the block reads back as NaN
   const float d = __half2float(__ushort_as_half(scale));
+  // round_half_even(x / d) without eight divisions.  x and d have at most 11
+  // significant bits and the quotient's half-integers h / 2 at most 8, so
+  // 2 x = h d or the two are 2^-19 apart, relative: x * (1 / d), off by less
+  // than 2^-22, rounds as the quotient does unless that is a half-integer
+  // exactly.  Then |x - q d| = d / 2 (an exact fma), and an odd q goes to its even neighbour.
+  const float inv = d > 0.f ? 1.f / d : 0.f;
   uint32_t u[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float r = d > 0.f ? fminf(fmaxf(rintf(x[j] / d), low), top) : 0.f;
-    u[j] = (uint32_t)((int)r + bias);
+    float q = rintf(x[j] * inv);
+    const float rest = fmaf(-q, d, x[j]);
+    if (fabsf(rest) * 2.f == d && q != 2.f * rintf(0.5f * q)) q += copysignf(1.f, rest);
+    q = d > 0.f ? fminf(fmaxf(q, low), top) : 0.f;
+    u[j] = (uint32_t)((int)q + bias);
   }
   if (BITS == 8)
     return make_uint2(u[0] | u[1] << 8 | u[2] << 16 | u[3] << 24, u[4] | u[5] << 8 | u[6] << 16 | u[7] << 24);
@@ -112,7 +121,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint16_t& scale)
 // LPR lanes a row.  NORM: q and k rows are normalised and rotated.  BITS > 0:
 // k and v rows go to the cache (else k goes to ko and there is no v).
 template <int LPR, bool BF16, bool NORM, int BITS>
-__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowArgs r, const KvArgs kv) {
+__global__ void __launch_bounds__(kRowThreads, 4) head_rows_kernel(const RowArgs r, const KvArgs kv) {
   constexpr bool STORE = BITS > 0;
   const int lane = threadIdx.x % LPR;
   const uint32_t unit = blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR;
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowArgs r,
     const int h = s + i * r.slots;
     if (i > 0 && i * r.slots >= H) break;  // uniform: no unit has an i-th row
     uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    if (NORM) {
+    if (NORM && __any_sync(0xffffffffu, h < r.nq + r.nk)) {
       float f[8], ss = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) unpack2<BF16>(w[j], f[2 * j], f[2 * j + 1]);
@@ -236,13 +245,13 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowArgs r,
         *reinterpret_cast<uint4*>(dst.p + (int64_t)t * dst.ts + hh * dst.hs + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    if (STORE) {
+    if (STORE && __any_sync(0xffffffffu, h >= r.nq)) {
       constexpr int B = STORE ? BITS : 8, R = kv_row_bytes(LPR * 8, B);
       float f[8];
       uint16_t scale;
 #pragma unroll
       for (int j = 0; j < 4; ++j) unpack2<BF16>(w[j], f[2 * j], f[2 * j + 1]);
-      const uint2 u = quantise8<B>(f, scale);  // every lane: shuffles
+      const uint2 u = quantise8<B>(f, scale);  // the whole warp: shuffles
       if (live && tile && h >= r.nq && h < H) {
         const bool is_v = h >= r.nq + r.nk;
         uint8_t* base = tile + (size_t)(h - r.nq - (is_v ? r.nk : 0)) * kv.head_bytes + (is_v ? kv_half_bytes(LPR * 8, B) : 0);
