@@ -1,651 +1,45 @@
-// Attention of a batch's new tokens over the quantised paged cache.
-//
-// attend_rows_kernel: few rows a sequence (decode, speculation).  Rows are
-// (new token, query head of the kv head's group), 8 * NT to a row tile.  A
-// call is a line of work units, one for each 32-token tile of keys that a
-// (sequence, kv head, row tile) segment has to see and kSegment for the
-// segment itself; the line is cut into equal parts, one a CTA, whatever the
-// lengths are.  A CTA's four warps take every fourth tile of a segment, each
-// with a ring of its own that one lane fills by bulk copies (half a tile, its
-// K or its V with the scales, is contiguous in the pool), and keep a running
-// maximum, sum and output in registers (one pass over the keys).  The warps'
-// results are merged in shared memory; a segment that ends in another CTA
-// leaves a partial result in the workspace and attend_join_kernel merges
-// those.
-//
-// The products run on mma.sync m16n8k16 with keys (or output elements) as M
-// and rows as N, so that a group of 8 query heads fills the tile: with rows
-// as M half of it was padding, and the warp instructions a tile went from
-// 1,112 to about 600, which is what bounds the 4-bit case.  S^T = K Q^T has its
-// probabilities transposed in registers (movmatrix) into the operand of
-// O^T = V^T P^T.
-//
-// Dequantisation happens on the way into the tensor core.  K: a lane's 8
-// elements of a 32-element block are the operands of two k16 steps (the order
-// of the reduction is free, so the natural byte order serves as the
-// fragment's), as exact fp16 integers (1024 + u through the exponent, minus
-// 1024 + bias); the block's scale multiplies the fp32 product.  V: a byte
-// permutation pairs the same element of two keys; integer times scale is
-// rounded to fp16 once.  Queries are scaled by a power of two per row so that
-// fp16 holds them whatever their range; probabilities carry 2^8 so that small
-// ones keep their precision in fp16.
-#include <cfloat>
-#include <cmath>
-
-#include "moe_kv.cuh"
-#include "moe_ptx.cuh"
+// Attention of a batch's new tokens over the quantised paged cache: the plan,
+// the merge of partial results and the C entries.  The kernels:
+//   attend_rows_kernel  (moe_attend_rows.cuh)   few rows a sequence, mma.sync
+//   attend_tiles_kernel (moe_attend_tiles.cuh)  many rows a sequence, tcgen05
+#include "moe_attend.cuh"
 
 namespace moe {
 namespace {
 
 using namespace ptx;
 
-constexpr int kAttWarps = 4;
-constexpr int kAttThreads = 32 * kAttWarps;
-// Units of work that a segment costs beside its tiles: its queries, its first
-// copy's latency, its merge.  Measured on 64 sequences of 1 to 24,001 tokens:
-// 73 us with 2, 54 with 4, 42 with 8 and 16; equal lengths do not notice.
-constexpr int kSegment = 12;
-constexpr int kMinUnits = 8;    // units a CTA takes at least
-constexpr float kPShift = 8.f;  // probabilities are held times 2^8
-constexpr uint32_t kNaN = 0x7FFFFFFFu;
+// Merges the partial results of the cut segments, the one that ends in part
+// blockIdx.x.  A lone long sequence has up to a hundred parts a segment: then
+// (WARPS 8) a CTA takes one row, its warps every eighth part; many segments
+// have a part or two each: then (WARPS 1) every warp takes a row.
+constexpr int kJoinThreads = 256;
 
-struct AttArgs {
-  const uint16_t* q;
-  int64_t q_ts, q_hs;
-  uint16_t* out;
-  int64_t o_ts, o_hs;
-  float* lse;
-  float scale_log2;  // scale * log2(e)
-  int nq, group;
-  int tile_rows, max_row_tiles;  // rows of a row tile; row tiles of the longest sequence
-  int parts;                     // CTAs of attend_rows_kernel
-  float* partial;                // [parts][2][tile_rows][D]
-  float2* stats;                 // [parts][2][tile_rows] (maximum, sum)
-  int64_t* starts;               // [segments]: where the segment's first tile lies on the line of work; [-1]: units a CTA takes
-};
-
-// A sequence as the kernels see it.
-struct Seq {
-  int row0, n, len, tiles, row_tiles;  // first row, new tokens, length, 32-token tiles of keys, row tiles
-  bool over;                           // longer than the block table is wide
-};
-
-__device__ __forceinline__ Seq seq_at(const KvArgs& a, const AttArgs& t, int b) {
-  Seq s;
-  s.row0 = __ldg(a.cu + b);
-  s.n = __ldg(a.cu + b + 1) - s.row0;
-  s.len = max(__ldg(a.lens + b), 0);
-  if (s.row0 < 0 || s.n < 0 || s.n > a.max_tokens || s.row0 > a.n_tokens - s.n) s.n = 0;  // flagged by flag_batch
-  const int cap = a.max_pages * a.page_size;
-  s.over = s.len > cap;
-  s.tiles = max(1, (min(s.len, cap) + kKvTile - 1) / kKvTile);
-  s.row_tiles = (s.n * t.group + t.tile_rows - 1) / t.tile_rows;
-  return s;
-}
-
-__device__ void flag_batch(const KvArgs& a, int b) {
-  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), len = __ldg(a.lens + b);
-  int bad = 0;
-  if (c0 < 0 || c1 < c0 || c1 - c0 > a.max_tokens || c1 > a.n_tokens || c1 - c0 > len) bad |= MOE_KV_BAD_BATCH;
-  if (len > a.max_pages * a.page_size) bad |= MOE_KV_BAD_PAGE;
-  if (bad) kv_flag(a, bad);
-}
-
-// Element j of lane group c's (0..7) share of the output: a contiguous run of
-// a key's bytes, or two for 8-bit heads of 256.
-template <int D, int BITS>
-__device__ __forceinline__ int out_dim(int j, int c) {
-  if (BITS == 8 && D == 256) return (j >> 4) * 128 + 16 * c + (j & 15);
-  return (D / 8) * c + j;
-}
-
-// Shared memory of attend_rows_kernel.  Three CTAs an SM where registers
-// (the output is D / 4 * NT of them) and the rings allow it, else two.
-template <int D, int BITS, int NT>
-struct RowsPlan {
-  static constexpr int kHalf = kv_half_bytes(D, BITS);
-  static constexpr int kBlocks = NT == 4 || D * NT >= 512 || (D == 256 && BITS == 8) ? 2 : 3;
-  static constexpr int kRingBytes = kBlocks == 2 ? 26112 : D == 256 ? 13824 : 17408;
-  static constexpr int kEntries = (kRingBytes / kHalf) < 12 ? (kRingBytes / kHalf) : 12;
-  static constexpr int kRing = kEntries * kHalf;          // bytes a warp
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kQBytes = kRows * D * 2;           // query fragments
-  static constexpr int kMerge = kRows * (D + 4) * 4;      // a warp's output for the merge, inside its ring
-  static constexpr int kSmem = kAttWarps * kRing + kQBytes + kRows * 4 + kAttWarps * kEntries * 8;
-  static_assert(kMerge <= kRing, "the merge buffer lies in the ring");
-  static_assert(kEntries >= 3, "a ring of three halves at least");
-};
-
-// (v & mask) | bits in one instruction; `bits` has to be a register (see kernel).
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "n"(MASK), "r"(bits));
-  return r;
-}
-
-// Eight stored integers of a key as the fp16 operand pairs of two k16 steps.
-// magic: 0x6400 in both halves, the fp16 exponent at which a mantissa step is 1.
-template <int BITS>
-__device__ __forceinline__ void key_operands(uint32_t (&k)[4], uint32_t at, uint32_t magic) {
-  if (BITS == 8) {
-    const uint2 w = lds64(at);
-    k[0] = hsub2(prmt(w.x, magic, 0x5150), 0x64806480u);
-    k[1] = hsub2(prmt(w.x, magic, 0x5352), 0x64806480u);
-    k[2] = hsub2(prmt(w.y, magic, 0x5150), 0x64806480u);
-    k[3] = hsub2(prmt(w.y, magic, 0x5352), 0x64806480u);
-  } else {
-    const uint32_t w = lds32(at), w8 = w >> 8;
-    k[0] = hsub2(and_or<0x000F000Fu>(w, magic), 0x64086408u);
-    k[1] = hfma2(and_or<0x00F000F0u>(w, magic), 0x2C002C00u, 0xD480D480u);
-    k[2] = hsub2(and_or<0x000F000Fu>(w8, magic), 0x64086408u);
-    k[3] = hfma2(and_or<0x00F000F0u>(w8, magic), 0x2C002C00u, 0xD480D480u);
-  }
-}
-
-// One warp's products of a 32-key tile: s[i][n] holds keys 16 i + g and
-// 16 i + 8 + g (g = lane / 4) against rows 8 n + 2 t and + 1 (t = lane % 4).
-template <int D, int BITS, int NT>
-__device__ __forceinline__ void score_tile(float (&s)[2][NT][4], uint32_t kb, uint32_t qf, int lane, uint32_t magic) {
-  constexpr int R = kv_row_bytes(D, BITS), NC = R / 16;
-  const int g = lane >> 2, t = lane & 3, turn = kv_turn(g) & (NC - 1);
-#pragma unroll
-  for (int b = 0; b < D / 32; ++b) {
-    uint4 q[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) q[n] = lds128(qf + ((b * NT + n) * 32 + lane) * 16);
-    const int at = BITS == 8 ? (((2 * b + (t >> 1)) ^ turn) << 4) + (t & 1) * 8 : ((b ^ turn) << 4) + t * 4;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t k0[4], k1[4];
-      key_operands<BITS>(k0, kb + (16 * i + g) * R + at, magic);
-      key_operands<BITS>(k1, kb + (16 * i + 8 + g) * R + at, magic);
-      const uint32_t sc = kb + kKvTile * R + (b * kKvTile + 16 * i + g) * 2;
-      const float d0 = __half2float(__ushort_as_half((uint16_t)lds16(sc)));
-      const float d1 = __half2float(__ushort_as_half((uint16_t)lds16(sc + 16)));
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float p[4];
-        mma_f16_zero(p, k0[0], k1[0], k0[1], k1[1], q[n].x, q[n].y);
-        mma_f16(p, k0[2], k1[2], k0[3], k1[3], q[n].z, q[n].w);
-        s[i][n][0] = b ? fmaf(p[0], d0, s[i][n][0]) : p[0] * d0;
-        s[i][n][1] = b ? fmaf(p[1], d0, s[i][n][1]) : p[1] * d0;
-        s[i][n][2] = b ? fmaf(p[2], d1, s[i][n][2]) : p[2] * d1;
-        s[i][n][3] = b ? fmaf(p[3], d1, s[i][n][3]) : p[3] * d1;
-      }
-    }
-  }
-}
-
-// o += p v for 16 keys (step u of a tile).  edge: keys from lim on (within
-// the tile) are seen by no row and count as 0 whatever their bytes say, and so
-// do non-finite scales (the caller deals with the rows that see them).
-template <int D, int BITS, int NT>
-__device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint32_t (&p)[NT][2], uint32_t vb, int u, int lane,
-                                           bool edge, int lim, uint32_t magic) {
-  constexpr int R = kv_row_bytes(D, BITS), NC = R / 16, RUN = D / 8;
-  constexpr int kRuns = (BITS == 8 && D == 256) ? 2 : 1;  // runs of RUN / kRuns elements a lane group has
-  constexpr int kWords = RUN / kRuns * BITS / 32;         // 32-bit words of a run: 1, 2 or 4
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int r = 0; r < kRuns; ++r) {
-    const int first = r * 128 + g * (RUN / kRuns);  // first element of the run
-    const int blk = first / 32;
-    uint32_t v[4][4], sc[2];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int key = 16 * u + 2 * t + (x & 1) + (x >> 1) * 8;
-      const int turn = kv_turn(key) & (NC - 1);
-      const int byte = first * BITS / 8;
-      const uint32_t a = vb + key * R + (((byte >> 4) ^ turn) << 4) + (byte & 15);
-      if (kWords == 4) {
-        const uint4 w = lds128(a);
-        v[x][0] = w.x, v[x][1] = w.y, v[x][2] = w.z, v[x][3] = w.w;
-      } else if (kWords == 2) {
-        const uint2 w = lds64(a);
-        v[x][0] = w.x, v[x][1] = w.y;
-      } else {
-        v[x][0] = lds32(a);
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int key = 16 * u + 2 * t + 8 * y;
-      sc[y] = lds32(vb + kKvTile * R + (blk * kKvTile + key) * 2);
-      if (edge) {
-        if (key >= lim || (sc[y] & 0x7C00u) == 0x7C00u) sc[y] &= 0xFFFF0000u;
-        if (key + 1 >= lim || (sc[y] & 0x7C000000u) == 0x7C000000u) sc[y] &= 0x0000FFFFu;
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-      // m-tiles of two elements each: a[0], a[1] keys 2t, 2t + 1 of the first and second; a[2], a[3] keys 2t + 8, 2t + 9
-      if (BITS == 8) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = prmt(v[0][w], v[1][w], h ? 0x7362 : 0x5140), y = prmt(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
-          uint32_t a[4];
-          a[0] = hmul2(hsub2(prmt(x, magic, 0x5150), 0x64806480u), sc[0]);
-          a[1] = hmul2(hsub2(prmt(x, magic, 0x5352), 0x64806480u), sc[0]);
-          a[2] = hmul2(hsub2(prmt(y, magic, 0x5150), 0x64806480u), sc[1]);
-          a[3] = hmul2(hsub2(prmt(y, magic, 0x5352), 0x64806480u), sc[1]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[r * 8 + 2 * w + h][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t x = prmt(v[0][w], v[1][w], q ? 0x7632 : 0x5410), y = prmt(v[2][w], v[3][w], q ? 0x7632 : 0x5410);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a[4];
-            a[0] = hmul2(hsub2(and_or<0x000F000Fu>(x, magic), 0x64086408u), sc[0]);
-            a[1] = hmul2(hfma2(and_or<0x00F000F0u>(x, magic), 0x2C002C00u, 0xD480D480u), sc[0]);
-            a[2] = hmul2(hsub2(and_or<0x000F000Fu>(y, magic), 0x64086408u), sc[1]);
-            a[3] = hmul2(hfma2(and_or<0x00F000F0u>(y, magic), 0x2C002C00u, 0xD480D480u), sc[1]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(o[4 * w + 2 * q + h][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
-            x >>= 8, y >>= 8;
-          }
-        }
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l) - kPShift) * 0.6931471805599453f;
-}
-
-template <int D, int BITS, bool BF16, int NT>
-__global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks)) attend_rows_kernel(const KvArgs a, const AttArgs t) {
-  using P = RowsPlan<D, BITS, NT>;
-  constexpr int R = kv_row_bytes(D, BITS), kRows = P::kRows;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t ring = smem_u32(smem) + warp * P::kRing;
-  float* merge = reinterpret_cast<float*>(smem);  // warp w's part starts at its ring
-  uint8_t* misc = smem + kAttWarps * P::kRing;
-  const uint32_t qf = smem_u32(misc);
-  uint4* qs = reinterpret_cast<uint4*>(misc);
-  float* row_exp = reinterpret_cast<float*>(misc + P::kQBytes);  // [kRows] 2^e of the query scaling
-  const uint32_t bars = smem_u32(misc + P::kQBytes + kRows * 4) + warp * P::kEntries * 8;
-  __shared__ long long s_sum[kAttWarps];
-  __shared__ long long s_base;
-  __shared__ int s_b;
-  __shared__ float2 s_stat[kAttWarps][kRows];
-
-  if (lane < P::kEntries) mbar_init(bars + lane * 8, 1);
-  fence_mbar_init();
-
-  // the line of work: each thread sums its share of the sequences
-  const int chunk = (a.n_seqs + kAttThreads - 1) / kAttThreads;
-  const int b_lo = min(tid * chunk, a.n_seqs), b_hi = min(b_lo + chunk, a.n_seqs);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const Seq s = seq_at(a, t, b);
-    mine += (long long)s.row_tiles * a.heads * (s.tiles + kSegment);
-    if (blockIdx.x == 0) flag_batch(a, b);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kAttWarps; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  const long long part = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinUnits);
-  const long long w0 = (long long)blockIdx.x * part, w1 = min(w0 + part, total);
-  if (blockIdx.x == 0 && tid == 0) t.starts[-1] = part;
-  if (w0 < total && before <= w0 && w0 < before + mine) {
-    s_base = before;
-    s_b = b_lo;
-  }
-  __syncthreads();
-  grid_launch_dependents();
-  if (w0 >= total) return;
-
-  int b = s_b;
-  long long base = s_base, cur = w0;
-  int in_slot = 0, out_slot = 0;  // the ring's next entry to fill and to use
-  uint32_t phase = 0;             // of the entry to use
-  bool timed_out = false;
-  // the exponent of the dequantisation in a register the compiler cannot see through: with two constants an
-  // and-or would take two instructions
-  uint32_t magic = 0x64006400u;
-  asm volatile("" : "+r"(magic));
-  const int g = lane >> 2, tq = lane & 3;
-  while (cur < w1) {
-    const Seq sq = seq_at(a, t, b);
-    const int units = sq.tiles + kSegment;
-    const long long size = (long long)sq.row_tiles * a.heads * units;
-    const long long local = cur - base;
-    if (local >= size) {
-      base += size;
-      ++b;
-      continue;
-    }
-    const int seg = (int)(local / units), u0 = (int)(local - (long long)seg * units);
-    const int u1 = (int)min((long long)units, u0 + (w1 - cur));
-    const int t0 = max(u0 - kSegment, 0), t1 = max(u1 - kSegment, 0);
-    cur += u1 - u0;
-    if (t1 <= t0) continue;  // the part ends before the segment's first tile
-    const int head = seg / sq.row_tiles, rt = seg - head * sq.row_tiles;
-    const int rows = min(kRows, sq.n * t.group - rt * kRows);
-
-    __syncthreads();  // the previous piece's merge has been read
-    fence_async_shared();
-    // this warp's tiles t0 + warp, + 4, ...; lane j holds the address of the (first + j)-th, and issues its copies
-    const int nt = (t1 - t0 - warp + kAttWarps - 1) / kAttWarps;
-    int first = 0;
-    const uint8_t* mine_src = nullptr;
-    bool bad_page = false;
-    auto load_pages = [&](int from) {
-      first = from;
-      const int i = from + lane;
-      if (i < nt) {
-        const int pos = (t0 + warp + kAttWarps * i) * kKvTile, pi = kv_page_of(a, pos);
-        int page = pi < a.max_pages ? __ldg(a.table + (size_t)b * a.table_stride + pi) : -1;
-        if ((unsigned)page >= (unsigned)a.n_pages) {
-          if (sq.len > 0) bad_page = true;  // an empty sequence's one tile holds nothing that is seen
-          page = 0;                         // in bounds; the rows become NaN
-        }
-        mine_src = a.data + (size_t)page * a.page_bytes + (size_t)head * a.head_bytes +
-                   (size_t)((pos - pi * a.page_size) / kKvTile) * (2 * P::kHalf);
-      }
-    };
-    int sent = 0;  // halves of this piece issued
-    auto issue = [&]() {
-      if (sent >= 2 * nt) return;
-      const int i = sent >> 1;
-      if (i >= first + 32) load_pages(i);
-      if (lane == i - first) {
-        mbar_expect_tx(bars + in_slot * 8, P::kHalf);
-        bulk_g2s(ring + in_slot * P::kHalf, mine_src + (sent & 1) * P::kHalf, P::kHalf, bars + in_slot * 8);
-      }
-      in_slot = in_slot + 1 == P::kEntries ? 0 : in_slot + 1;
-      ++sent;
-    };
-    // Gives the slot just read back to the producer and moves on.
-    auto release = [&]() {
-      if (++out_slot == P::kEntries) out_slot = 0, phase ^= 1;
-      __syncwarp();
-      issue();
-    };
-    load_pages(0);
-    for (int e = 0; e < P::kEntries; ++e) issue();
-
-    // Queries: D / 8 threads a row, 8 elements each, in the order of the
-    // operand pairs.  The row's largest magnitude sets the power of two it is
-    // divided by; a negative scale goes into the sign (and 0 into the query), so that the scores' factor is positive.
-    {
-      constexpr int TPR = D / 8;
-#pragma unroll
-      for (int r0 = 0; r0 < kRows; r0 += kAttThreads / TPR) {
-        const int row = r0 + tid / TPR, d8 = tid % TPR;
-        const int fr = rt * kRows + row, tok = fr / t.group, gh = fr - tok * t.group;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (row < rows)
-          w = *reinterpret_cast<const uint4*>(t.q + (int64_t)(sq.row0 + tok) * t.q_ts + (int64_t)(head * t.group + gh) * t.q_hs + d8 * 8);
-        float f[8];
-        unpack2<BF16>(w.x, f[0], f[1]);
-        unpack2<BF16>(w.y, f[2], f[3]);
-        unpack2<BF16>(w.z, f[4], f[5]);
-        unpack2<BF16>(w.w, f[6], f[7]);
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(f[i]));
-#pragma unroll
-        for (int o = 1; o < TPR; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        // exponent of the largest: |f| * 2^-e stays below 2 (2^8 at the end of bf16's range); infinities and NaN stay what they are
-        int e = ((__float_as_uint(big) >> 23) & 255) - 127;
-        e = big > 0.f && e < 128 ? min(max(e, -120), 120) : 0;
-        float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (t.scale_log2 < 0.f) down = -down;
-        if (t.scale_log2 == 0.f) down = 0.f;
-        if (row < kRows) {
-          if (d8 == 0) row_exp[row] = __uint_as_float((uint32_t)(127 + e) << 23);
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            h[j] = BITS == 8 ? pack2<false>(f[2 * j] * down, f[2 * j + 1] * down) : pack2<false>(f[j] * down, f[j + 4] * down);
-          qs[((d8 >> 2) * NT + (row >> 3)) * 32 + (row & 7) * 4 + (d8 & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
-        }
-      }
-    }
-    __syncthreads();
-
-    float o[D / 16][NT][4], m[NT][2], l[NT][2], c[NT][2];
-    int see[NT][2];  // last position that the lane's rows see; rows that are none see nothing
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 8 * n + 2 * tq + h;
-        m[n][h] = -INFINITY;
-        l[n][h] = 0.f;
-        c[n][h] = t.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(t.scale_log2) * row_exp[row], FLT_MIN);
-        see[n][h] = row < rows ? sq.len - sq.n + (rt * kRows + row) / t.group : -1;
-      }
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][n][i] = 0.f;
-    const int see_min = sq.len - sq.n + (rt * kRows) / t.group;
-    const int see_max = sq.len - sq.n + (rt * kRows + rows - 1) / t.group;
-
-    for (int i = 0; i < nt; ++i) {
-      const int key0 = (t0 + warp + kAttWarps * i) * kKvTile;
-      const bool edge = key0 + kKvTile - 1 > see_min;
-      float s[2][NT][4];
-      {
-        if (!mbar_wait(bars + out_slot * 8, phase)) timed_out = true;
-        score_tile<D, BITS, NT>(s, ring + out_slot * P::kHalf, qf, lane, magic);
-        release();
-      }
-      if (edge) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int key = key0 + 16 * x + g;
-            if (key > see[n][0]) s[x][n][0] = -INFINITY;
-            if (key > see[n][1]) s[x][n][1] = -INFINITY;
-            if (key + 8 > see[n][0]) s[x][n][2] = -INFINITY;
-            if (key + 8 > see[n][1]) s[x][n][3] = -INFINITY;
-          }
-      }
-      // maxima in units of log2 (c > 0, so the largest product has the largest score)
-      float top[NT][2];
-      bool grew = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v = fmaxf(fmaxf(s[0][n][h], s[0][n][h + 2]), fmaxf(s[1][n][h], s[1][n][h + 2]));
-#pragma unroll
-          for (int of = 4; of < 32; of <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, of));
-          top[n][h] = v * c[n][h];
-          grew |= top[n][h] > m[n][h];
-        }
-      if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float r[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool up = top[n][h] > m[n][h];
-            r[h] = up ? ex2(m[n][h] - top[n][h]) : 1.f;
-            if (up) m[n][h] = top[n][h];
-            l[n][h] *= r[h];
-          }
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            o[j][n][0] *= r[0], o[j][n][1] *= r[1], o[j][n][2] *= r[0], o[j][n][3] *= r[1];
-          }
-        }
-      }
-      uint32_t p[2][NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float z0 = kPShift - (m[n][0] == -INFINITY ? 0.f : m[n][0]), z1 = kPShift - (m[n][1] == -INFINITY ? 0.f : m[n][1]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float e[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) e[h] = ex2(fmaf(s[x][n][h], c[n][h & 1], h & 1 ? z1 : z0));
-          l[n][0] += e[0] + e[2];
-          l[n][1] += e[1] + e[3];
-          p[x][n][0] = transpose8(pack2<false>(e[0], e[1]));
-          p[x][n][1] = transpose8(pack2<false>(e[2], e[3]));
-        }
-      }
-      {
-        if (!mbar_wait(bars + out_slot * 8, phase)) timed_out = true;
-        const uint32_t vb = ring + out_slot * P::kHalf;
-        const int lim = see_max + 1 - key0;
-        value_step<D, BITS, NT>(o, p[0], vb, 0, lane, edge, lim, magic);
-        value_step<D, BITS, NT>(o, p[1], vb, 1, lane, edge, lim, magic);
-        if (edge) {
-          // value_step took non-finite scales for 0, so that rows that do not see such a key stay clean; the rows that do become NaN
-          bool odd = false;
-          for (int blk = 0; blk < D / 32; ++blk) odd |= (lds16(vb + kKvTile * R + (blk * kKvTile + lane) * 2) & 0x7C00u) == 0x7C00u;
-          unsigned keys = __ballot_sync(0xffffffffu, odd && lane < lim);
-          while (keys) {
-            const int key = key0 + __ffs(keys) - 1;
-            keys &= keys - 1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (key <= see[n][h]) l[n][h] = __uint_as_float(kNaN);
-          }
-        }
-        release();
-      }
-    }
-    bool spoiled = false;
-    if (__any_sync(0xffffffffu, bad_page) || sq.over) {
-      if (lane == 0) kv_flag(a, MOE_KV_BAD_PAGE);
-      spoiled = true;
-    }
-    if (timed_out) {
-      if (lane == 0) kv_flag(a, MOE_KV_TIMEOUT);
-      spoiled = true;
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int of = 4; of < 32; of <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], of);
-        if (spoiled) l[n][h] = __uint_as_float(kNaN);
-        if (g == 0) s_stat[warp][8 * n + 2 * tq + h] = make_float2(m[n][h], l[n][h]);
-      }
-
-    // merge: the ring is drained (every half issued was used)
-    float* mine_o = merge + warp * (P::kRing / 4);
-    __syncwarp();
-    if (nt > 0) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < D / 16; j += 2)
-            *reinterpret_cast<float4*>(mine_o + (8 * n + 2 * tq + h) * (D + 4) + out_dim<D, BITS>(2 * j, g)) =
-                make_float4(o[j][n][h], o[j][n][h + 2], o[j + 1][n][h], o[j + 1][n][h + 2]);
-    }
-    __syncthreads();
-    {
-      constexpr int TPR = kAttThreads / kRows, NE = D / TPR;  // threads a row, elements a thread
-      const int row = tid / TPR, sub = tid % TPR;
-      float mm = -INFINITY, ll = 0.f, wgt[kAttWarps];
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) mm = fmaxf(mm, s_stat[w][row].x);
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) {
-        const float2 st = s_stat[w][row];
-        wgt[w] = st.x == -INFINITY ? 0.f : ex2(st.x - mm);
-        ll += st.y != st.y ? st.y : st.y * wgt[w];
-      }
-      const bool whole = t0 == 0 && t1 == sq.tiles;
-      const int fr = rt * kRows + row, tok = fr / t.group, gh = fr - tok * t.group;
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;
-      const size_t at = ((size_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * kRows + row;
-      if (row < rows) {
-#pragma unroll
-        for (int i = 0; i < NE; i += 4) {
-          const int d = sub * 4 + i * TPR;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < kAttWarps; ++w) {
-            if (w >= t1 - t0) break;  // that warp had no tile
-            const float4 v = *reinterpret_cast<const float4*>(merge + w * (P::kRing / 4) + row * (D + 4) + d);
-            acc.x = fmaf(wgt[w], v.x, acc.x);
-            acc.y = fmaf(wgt[w], v.y, acc.y);
-            acc.z = fmaf(wgt[w], v.z, acc.z);
-            acc.w = fmaf(wgt[w], v.w, acc.w);
-          }
-          if (whole)
-            *reinterpret_cast<uint2*>(t.out + (int64_t)(sq.row0 + tok) * t.o_ts + (int64_t)(head * t.group + gh) * t.o_hs + d) =
-                make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-          else
-            *reinterpret_cast<float4*>(t.partial + at * D + d) = acc;
-        }
-        if (sub == 0) {
-          if (!whole)
-            t.stats[at] = make_float2(mm, ll);
-          else if (t.lse)
-            t.lse[(int64_t)(sq.row0 + tok) * t.nq + head * t.group + gh] = lse_of(mm, ll);
-        }
-      }
-      if (t0 == 0 && tid == 0) t.starts[((int64_t)b * a.heads + head) * t.max_row_tiles + rt] = cur - (u1 - u0) + (kSegment - u0);
-    }
-  }
-}
-
-// Merges the partial results of the segments that several CTAs worked on:
-// one CTA a row, its warps every eighth part, four parts' loads in flight (a
-// lone long sequence has up to a hundred parts a segment).
-constexpr int kJoinWarps = 8;
-constexpr int kJoinThreads = 32 * kJoinWarps;
-
-template <int D, bool BF16>
+template <int D, bool BF16, int WARPS>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const KvArgs a, const AttArgs t) {
   constexpr int NE = D / 32;  // elements a lane holds
-  __shared__ float s_o[kJoinWarps][D];
-  __shared__ float2 s_stat[kJoinWarps];
+  __shared__ float s_o[WARPS > 1 ? WARPS : 1][D];
+  __shared__ float2 s_stat[WARPS > 1 ? WARPS : 1];
   grid_wait();
-  const int seg = blockIdx.x, row = blockIdx.y;
-  const int rt = seg % t.max_row_tiles, bh = seg / t.max_row_tiles, head = bh % a.heads, b = bh / a.heads;
-  const Seq sq = seq_at(a, t, b);
-  if (rt >= sq.row_tiles || rt * t.tile_rows + row >= sq.n * t.group) return;
-  const long long part = t.starts[-1], start = t.starts[seg];
-  const int c0 = (int)(start / part), c1 = (int)((start + sq.tiles - 1) / part);
-  if (c0 == c1) return;  // one CTA had it all
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // a part that begins at the segment's first tile lies in its CTA's slot 1, the others in slot 0
+  const SegmentEnd end = t.ends[blockIdx.x];
+  if (end.first < 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = WARPS > 1 ? tid >> 5 : 0;
+  const int row = WARPS > 1 ? blockIdx.y : blockIdx.y * (kJoinThreads / 32) + (tid >> 5);
+  const int c0 = end.first, c1 = blockIdx.x, head = end.head;
+  const Seq sq = seq_at(a, end.b);
+  const int fr = end.rt * t.tile_rows + row;
+  if (row >= t.tile_rows || fr >= sq.n * t.group) return;
+  // the part that begins at the segment's first tile lies in its CTA's slot 1, the others in slot 0; four parts' loads in flight
   float m = -INFINITY, l = 0.f, o[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) o[i] = 0.f;
   constexpr int kAhead = 4;
-  for (int c = c0 + warp; c <= c1; c += kJoinWarps * kAhead) {
+  for (int c = c0 + warp; c <= c1; c += WARPS * kAhead) {
     float2 st[kAhead];
     float v[kAhead][NE];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int ck = c + k * kJoinWarps;
+      const int ck = c + k * WARPS;
       st[k] = make_float2(-INFINITY, 0.f);
       if (ck > c1) continue;
       const size_t at = ((size_t)ck * 2 + (ck == c0 ? 1 : 0)) * t.tile_rows + row;
@@ -656,7 +50,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const KvArgs 
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (c + k * kJoinWarps > c1) break;
+      if (c + k * WARPS > c1) break;
       const float n = fmaxf(m, st[k].x);
       const float wo = m == -INFINITY ? 0.f : ex2(m - n), wn = st[k].x == -INFINITY ? 0.f : ex2(st[k].x - n);
       l = (l != l ? l : l * wo) + (st[k].y != st[k].y ? st[k].y : st[k].y * wn);
@@ -665,63 +59,64 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const KvArgs 
       m = n;
     }
   }
-#pragma unroll
-  for (int i = 0; i < NE; ++i) s_o[warp][lane * NE + i] = o[i];
-  if (lane == 0) s_stat[warp] = make_float2(m, l);
-  __syncthreads();
-  float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, s_stat[w].x);
-  float wgt[kJoinWarps];
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    wgt[w] = s_stat[w].x == -INFINITY ? 0.f : ex2(s_stat[w].x - mm);
-    ll += s_stat[w].y != s_stat[w].y ? s_stat[w].y : s_stat[w].y * wgt[w];
-  }
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;
-  const int fr = rt * t.tile_rows + row, tok = fr / t.group, gh = fr - tok * t.group;
+  const int tok = fr / t.group, gh = fr - tok * t.group;
   uint16_t* dst = t.out + (int64_t)(sq.row0 + tok) * t.o_ts + (int64_t)(head * t.group + gh) * t.o_hs;
-  for (int d = 2 * tid; d < D; d += 2 * kJoinThreads) {
-    float v0 = 0.f, v1 = 0.f;
+  float* lse = t.lse ? t.lse + (int64_t)(sq.row0 + tok) * t.nq + head * t.group + gh : nullptr;
+  if constexpr (WARPS == 1) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      v0 = fmaf(wgt[w], s_o[w][d], v0);
-      v1 = fmaf(wgt[w], s_o[w][d + 1], v1);
+    for (int i = 0; i < NE; i += 2) *reinterpret_cast<uint32_t*>(dst + lane * NE + i) = pack2<BF16>(o[i] * inv, o[i + 1] * inv);
+    if (lse && lane == 0) *lse = lse_of(m, l);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s_o[warp][lane * NE + i] = o[i];
+    if (lane == 0) s_stat[warp] = make_float2(m, l);
+    __syncthreads();
+    float mm = -INFINITY, ll = 0.f, wgt[WARPS];
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_stat[w].x);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      wgt[w] = s_stat[w].x == -INFINITY ? 0.f : ex2(s_stat[w].x - mm);
+      ll += s_stat[w].y != s_stat[w].y ? s_stat[w].y : s_stat[w].y * wgt[w];
     }
-    *reinterpret_cast<uint32_t*>(dst + d) = pack2<BF16>(v0 * inv, v1 * inv);
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    for (int d = 2 * tid; d < D; d += 2 * kJoinThreads) {
+      float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        v0 = fmaf(wgt[w], s_o[w][d], v0);
+        v1 = fmaf(wgt[w], s_o[w][d + 1], v1);
+      }
+      *reinterpret_cast<uint32_t*>(dst + d) = pack2<BF16>(v0 * inv, v1 * inv);
+    }
+    if (lse && tid == 0) *lse = lse_of(mm, ll);
   }
-  if (t.lse && tid == 0) t.lse[(int64_t)(sq.row0 + tok) * t.nq + head * t.group + gh] = lse_of(mm, ll);
 }
 
 struct Workspace {
-  size_t partial, stats, starts, bytes;
+  size_t partial, stats, ends, bytes;
 };
 
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
-Workspace plan_workspace(int parts, int tile_rows, int dim, int64_t segments) {
+Workspace plan_workspace(int parts, int tile_rows, int dim) {
   Workspace w{};
   w.partial = 0;
   w.stats = up16(w.partial + (size_t)parts * 2 * tile_rows * dim * 4);
-  w.starts = up16(w.stats + (size_t)parts * 2 * tile_rows * 8);
-  w.bytes = up16(w.starts + 16 + (size_t)segments * 8);
+  w.ends = up16(w.stats + (size_t)parts * 2 * tile_rows * 8);
+  w.bytes = up16(w.ends + (size_t)parts * sizeof(SegmentEnd));
   return w;
 }
 
-template <typename K>
-bool raise_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
-template <int D, int BITS, bool BF16, int NT>
-moe_status_t launch_rows_kernel(const KvArgs& kv, const AttArgs& t, int64_t segments, cudaStream_t st) {
-  constexpr int smem = RowsPlan<D, BITS, NT>::kSmem;
-  if (!raise_smem(attend_rows_kernel<D, BITS, BF16, NT>, smem)) return MOE_ERR_CUDA;
-  attend_rows_kernel<D, BITS, BF16, NT><<<t.parts, kAttThreads, smem, st>>>(kv, t);
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+template <int D, bool BF16>
+moe_status_t launch_join_type(const KvArgs& kv, const AttArgs& t, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  const int64_t rows = (int64_t)kv.max_tokens * t.group;
-  cfg.gridDim = dim3((unsigned)segments, (unsigned)(rows < t.tile_rows ? rows : t.tile_rows));
+  const int64_t most = (int64_t)kv.max_tokens * t.group;
+  const int rows = (int)(most < t.tile_rows ? most : t.tile_rows);
+  const int64_t segments = (int64_t)kv.n_seqs * kv.heads * ((most + t.tile_rows - 1) / t.tile_rows);
+  const bool wide = t.parts >= 8 * segments || t.tile_rows <= 32;
+  cfg.gridDim = dim3((unsigned)t.parts, (unsigned)(wide ? rows : (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -729,31 +124,20 @@ moe_status_t launch_rows_kernel(const KvArgs& kv, const AttArgs& t, int64_t segm
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, BF16>, kv, t) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, attend_join_kernel<D, BF16, 8>, kv, t)
+                             : cudaLaunchKernelEx(&cfg, attend_join_kernel<D, BF16, 1>, kv, t);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
-
-// Rows of a row tile: 8 while they suffice, then 16 and 32, which share the
-// dequantised keys and values; heads of 256 have registers for 16.
-int rows_of_tile(int dim, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32; }
-
-template <int D, int BITS, bool BF16>
-moe_status_t launch_rows_tile(const KvArgs& kv, const AttArgs& t, int64_t segments, cudaStream_t st) {
-  if (t.tile_rows == 8) return launch_rows_kernel<D, BITS, BF16, 1>(kv, t, segments, st);
-  if constexpr (D < 256)
-    if (t.tile_rows == 32) return launch_rows_kernel<D, BITS, BF16, 4>(kv, t, segments, st);
-  return launch_rows_kernel<D, BITS, BF16, 2>(kv, t, segments, st);
-}
-
-template <int D, int BITS>
-moe_status_t launch_rows_type(const KvArgs& kv, const AttArgs& t, int64_t segments, bool bf16, cudaStream_t st) {
-  return bf16 ? launch_rows_tile<D, BITS, true>(kv, t, segments, st) : launch_rows_tile<D, BITS, false>(kv, t, segments, st);
+template <int D>
+moe_status_t launch_join(const KvArgs& kv, const AttArgs& t, bool bf16, cudaStream_t st) {
+  return bf16 ? launch_join_type<D, true>(kv, t, st) : launch_join_type<D, false>(kv, t, st);
 }
 
 // What both entries derive from their arguments.
 struct AttPlan {
   KvArgs kv;
-  int parts, tile_rows, row_tiles;
-  int64_t segments;
+  bool tiles;  // attend_tiles_kernel
+  int parts, tile_rows;
   Workspace ws;
 };
 
@@ -764,19 +148,31 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   if (shared_tokens / cache->page_size > batch->max_pages) return MOE_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)batch->max_tokens * (n_q / cache->n_kv_heads);
   if (rows > 1 << 24) return MOE_ERR_UNSUPPORTED;
-  p->tile_rows = rows_of_tile(cache->head_dim, rows);
-  p->row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
-  p->segments = (int64_t)batch->n_seqs * cache->n_kv_heads * p->row_tiles;
-  if (p->segments > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   int sms = 0;
   st = device_sms(&sms);
   if (st != MOE_OK) return st;
-  p->parts = sms * (p->tile_rows == 32 || cache->head_dim * p->tile_rows >= 4096 || (cache->head_dim == 256 && cache->bits == 8) ? 2 : 3);
-  p->ws = plan_workspace(p->parts, p->tile_rows, cache->head_dim, p->segments);
+  // A sequence's rows in tiles of 8 while they suffice, then 16 and 32, which
+  // share the dequantised keys and values (heads of 256 have registers for 16);
+  // above 64 rows the tensor cores' tiles of 256 (128 for heads of 256).
+  p->tiles = rows > 64;
+  if (p->tiles) {
+    p->tile_rows = cache->head_dim == 256 ? 128 : 256;
+    p->parts = sms;
+  } else {
+    p->tile_rows = rows <= 8 ? 8 : rows <= 16 || cache->head_dim == 256 ? 16 : 32;
+    p->parts = sms * rows_blocks(cache->head_dim, cache->bits, p->tile_rows);
+  }
+  p->ws = plan_workspace(p->parts, p->tile_rows, cache->head_dim);
   return MOE_OK;
 }
 
 }  // namespace
+
+// As RowsPlan::kBlocks.
+int rows_blocks(int dim, int bits, int tile_rows) {
+  return tile_rows == 32 || dim * tile_rows >= 4096 || (dim == 256 && bits == 8) ? 2 : 3;
+}
+
 }  // namespace moe
 
 extern "C" MOE_API moe_status_t moe_kv_attend_workspace(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t n_q,
@@ -816,19 +212,17 @@ extern "C" MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const
   t.nq = n_q;
   t.group = n_q / cache->n_kv_heads;
   t.tile_rows = p.tile_rows;
-  t.max_row_tiles = p.row_tiles;
   t.parts = p.parts;
   t.partial = (float*)(w + p.ws.partial);
   t.stats = (float2*)(w + p.ws.stats);
-  t.starts = (int64_t*)(w + p.ws.starts + 16);
+  t.ends = (moe::SegmentEnd*)(w + p.ws.ends);
   const bool bf = dtype == MOE_BF16;
   const cudaStream_t s = (cudaStream_t)cuda_stream;
-  if (cache->bits == 8) {
-    if (dim == 64) return moe::launch_rows_type<64, 8>(p.kv, t, p.segments, bf, s);
-    if (dim == 128) return moe::launch_rows_type<128, 8>(p.kv, t, p.segments, bf, s);
-    return moe::launch_rows_type<256, 8>(p.kv, t, p.segments, bf, s);
-  }
-  if (dim == 64) return moe::launch_rows_type<64, 4>(p.kv, t, p.segments, bf, s);
-  if (dim == 128) return moe::launch_rows_type<128, 4>(p.kv, t, p.segments, bf, s);
-  return moe::launch_rows_type<256, 4>(p.kv, t, p.segments, bf, s);
+  const auto launch = p.tiles ? (cache->bits == 8 ? moe::launch_tiles8 : moe::launch_tiles4)
+                              : (cache->bits == 8 ? moe::launch_rows8 : moe::launch_rows4);
+  const moe_status_t main_st = launch(p.kv, t, dim, bf, s);
+  if (main_st != MOE_OK) return main_st;
+  if (dim == 64) return moe::launch_join<64>(p.kv, t, bf, s);
+  if (dim == 128) return moe::launch_join<128>(p.kv, t, bf, s);
+  return moe::launch_join<256>(p.kv, t, bf, s);
 }

@@ -1,0 +1,602 @@
+// Attention with many rows a sequence (prefill chunks) on the tensor cores.
+//
+// A CTA holds NRT row tiles of 128 rows (new token, query head of the kv
+// head's group) and walks the keys 64 at a time:
+//   loader (1 warp)     bulk copies of the pool's half tiles (32 keys' K or V
+//                       with their scales) into a ring
+//   dequantise (4)      integer times scale, rounded to fp16 once, into
+//                       128-byte swizzled stages: K as the K-major and V, which
+//                       has the same rows, as the MN-major operand
+//   issue (1)           S = Q K^T (tcgen05.mma, fp32 in tensor memory, two
+//                       buffers a row tile), O += P V with P read from tensor memory
+//   softmax (4 a tile)  a thread a row: maximum, exponentials, sum; P goes
+//                       back into S's columns as fp16 (times 2^8, as in
+//                       attend_rows_kernel).  O is rescaled in tensor memory
+//                       only when a maximum grew by more than 2^7 since the
+//                       last time, which keeps P below fp16's largest.
+// The two row tiles share the dequantised keys and keep the tensor core busy
+// while the other's softmax runs.  Per 64 keys (heads of 128) the tensor core
+// needs about 1,000 cycles, the four schedulers 300 issue slots for the
+// dequantisation and 800 for the softmax: they bound it together.
+//
+// The line of work is measured in keys, causal limits included, so that all
+// parts cost the same: row tile rt of a sequence costs kSegmentKeys + the keys
+// in front of its new tokens + (rt + 1) * rows / group, in units of 1 / group.
+//
+// 4-bit elements leave the dequantisation in the order 0 4 1 5 2 6 3 7 within
+// each eight; queries are stored in the same order, and the output's is undone
+// when it is written.
+#pragma once
+
+#include "moe_attend.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int kKeys = 64;           // keys of a step
+constexpr int kSegmentKeys = 512;   // what a segment costs beside its keys, in keys
+constexpr float kGrow = 7.f;        // log2 by which a maximum may outgrow its reference
+constexpr int kDeqWarps = 4;
+
+template <int D, int BITS>
+struct TilesPlan {
+  static constexpr int NRT = D == 256 ? 1 : 2;
+  static constexpr int kRows = 128 * NRT;
+  static constexpr int kHalf = kv_half_bytes(D, BITS);
+  static constexpr int kEntries = D == 256 ? (BITS == 8 ? 6 : 8) : 12;  // half tiles in the raw ring
+  static constexpr int kStage = kKeys * D * 2;
+  static constexpr int kVStages = D == 256 ? 1 : 2;
+  static constexpr int kQ = 128 * D * 2;
+  static constexpr int kOffK = NRT * kQ;
+  static constexpr int kOffV = kOffK + 2 * kStage;
+  static constexpr int kOffRaw = kOffV + kVStages * kStage;
+  static constexpr int kOffBar = (kOffRaw + kEntries * kHalf + 15) & ~15;
+  // barriers: raw full and empty, K full and empty, V full and empty, Q full, S full, P full, O done
+  static constexpr int kBars = 2 * kEntries + 4 + 2 * kVStages + NRT * 6;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;
+  static constexpr int kSmem = kOffMisc + 64;
+  static constexpr int kSoftWarps = 4 * NRT;
+  static constexpr int kThreads = 32 * (kSoftWarps + kDeqWarps + 2);
+  static constexpr int kTmemO = NRT * 2 * kKeys;  // S buffers first, then O
+  static constexpr int kTmemCols = kTmemO + NRT * D <= 256 ? 256 : 512;
+  static_assert(kSmem <= 232448, "shared memory of an SM");
+  static_assert(kTmemO + NRT * D <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"(acc)
+               : "memory");
+}
+// A from tensor memory: two fp16 of a row in each 32-bit column.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(acc)
+               : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptors, 128-byte swizzle.  K-major: rows of 64
+// fp16, 8-row atoms 1,024 B apart.  MN-major: the same bytes with the 64 fp16
+// along N, K groups of 8 rows 1,024 B apart and the next 64 of N a panel away.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t panel) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16: D fp32, A and B fp16, M = 128, N; B MN-major when asked.
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// A part of a segment: key steps t0 .. t1 of row tile rt.
+struct Piece {
+  int b, head, rt, t0, t1, steps;
+  Seq sq;
+  int first_part;  // the CTA that has step 0
+};
+
+// The CTA's share of the line of work.
+template <int ROWS>
+struct Walk {
+  long long part, w1, cur, base;
+  int b;
+
+  // Cost of a head's row tiles 0 .. rt - 1, in keys times the group.
+  static __device__ __forceinline__ long long cost(const AttArgs& t, const Seq& s, long long rt) {
+    return rt * t.group * (kSegmentKeys + (long long)max(s.len - s.n, 0)) + (long long)ROWS * rt * (rt + 1) / 2;
+  }
+  static __device__ __forceinline__ int row_tiles(const AttArgs& t, const Seq& s) { return (s.n * t.group + ROWS - 1) / ROWS; }
+
+  __device__ bool next(const KvArgs& a, const AttArgs& t, Piece& p) {
+    while (cur < w1) {
+      const Seq s = seq_at(a, b);
+      const int n_rt = row_tiles(t, s);
+      const long long per_head = cost(t, s, n_rt), local = cur - base;
+      if (local >= per_head * a.heads) {
+        base += per_head * a.heads;
+        ++b;
+        continue;
+      }
+      const int head = (int)(local / per_head);
+      const long long x = local - head * per_head;
+      int lo = 0, hi = n_rt - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cost(t, s, mid) <= x)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const long long c0 = cost(t, s, lo), all = cost(t, s, lo + 1) - c0;
+      const long long x0 = x - c0, x1 = min(all, x0 + (w1 - cur)), seg_start = cur - x0;
+      cur += x1 - x0;
+      // the keys that the tile's last row sees
+      const int last = min((lo + 1) * ROWS, s.n * t.group) - 1;
+      const int lim = min(min(s.len - s.n + last / t.group + 1, s.len), a.max_pages * a.page_size);
+      p.steps = max(1, (lim + kKeys - 1) / kKeys);
+      auto step_at = [&](long long pos) {
+        const long long u = pos / t.group - kSegmentKeys;
+        return (int)min((long long)p.steps, (max(u, 0ll) + kKeys - 1) / kKeys);
+      };
+      p.t0 = step_at(x0);
+      p.t1 = x1 == all ? p.steps : step_at(x1);
+      if (p.t1 <= p.t0) continue;
+      p.b = b;
+      p.head = head;
+      p.rt = lo;
+      p.sq = s;
+      p.first_part = (int)((seg_start + min((long long)t.group * (kSegmentKeys + 1), all) - 1) / part);
+      return true;
+    }
+    return false;
+  }
+};
+
+// 32 keys' integers times scales into rows key_base .. of a stage.  V: keys
+// from lim on (within the half) are seen by no row and become 0, and so do
+// blocks of non-finite scale; the first such key's position goes to `bad`.
+template <int D, int BITS>
+__device__ __forceinline__ void dequantise_half(uint32_t raw, uint32_t stage, int key_base, int tid, bool is_v, int lim, int pos0,
+                                                int* bad, uint32_t magic) {
+  constexpr int R = kv_row_bytes(D, BITS), UPR = R / 16, EPU = 128 / BITS;  // 16-byte units a row, elements a unit
+  const int key = tid & 31, row = key_base + key, turn = kv_turn(key) & (UPR - 1);
+#pragma unroll
+  for (int c0 = 0; c0 < UPR; c0 += kDeqWarps) {
+    const int c = c0 + (tid >> 5);
+    if (UPR % kDeqWarps && c >= UPR) break;
+    const uint4 w4 = lds128(raw + key * R + ((c ^ turn) << 4));
+    uint32_t sc = lds16(raw + kKvTile * R + ((c * EPU / 32) * kKvTile + key) * 2);
+    if (is_v) {
+      if (key >= lim) {
+        sc = 0;
+      } else if ((sc & 0x7C00u) == 0x7C00u) {
+        sc = 0;
+        atomicMin(bad, pos0 + key);
+      }
+    }
+    const uint32_t s2 = prmt(sc, sc, 0x1010);
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int i = 0; i < EPU / 8; ++i) {
+      uint32_t h[4];
+      if (BITS == 8) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          h[2 * j] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5150), 0x64806480u), s2);
+          h[2 * j + 1] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5352), 0x64806480u), s2);
+        }
+      } else {
+        const uint32_t v = w[i], v8 = v >> 8;
+        h[0] = hmul2(hsub2(and_or<0x000F000Fu>(v, magic), 0x64086408u), s2);
+        h[1] = hmul2(hfma2(and_or<0x00F000F0u>(v, magic), 0x2C002C00u, 0xD480D480u), s2);
+        h[2] = hmul2(hsub2(and_or<0x000F000Fu>(v8, magic), 0x64086408u), s2);
+        h[3] = hmul2(hfma2(and_or<0x00F000F0u>(v8, magic), 0x2C002C00u, 0xD480D480u), s2);
+      }
+      const int oc = c * (EPU / 8) + i;  // chunk of 8 elements
+      sts128(stage + (oc >> 3) * (kKeys * 128) + row * 128 + (((oc & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+template <int D, int BITS, bool BF16>
+__global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tiles_kernel(const KvArgs a, const AttArgs t) {
+  using P = TilesPlan<D, BITS>;
+  constexpr int NRT = P::NRT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sm = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](int i) { return sm + P::kOffBar + 8 * i; };
+  constexpr int kRawFull = 0, kRawEmpty = P::kEntries, kKFull = 2 * P::kEntries, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
+                kVEmpty = kVFull + P::kVStages, kQFull = kVEmpty + P::kVStages, kSFull = kQFull + NRT, kPFull = kSFull + 2 * NRT,
+                kODone = kPFull + 2 * NRT;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P::kOffMisc);
+  int* s_bad = reinterpret_cast<int*>(smem + P::kOffMisc + 16);  // [8], by piece: position of the first bad page or non-finite V
+  __shared__ long long s_sum[16];
+  __shared__ long long s_base;
+  __shared__ int s_b;
+
+  if (tid == 0) {
+    for (int i = 0; i < P::kEntries; ++i) {
+      mbar_init(bar(kRawFull + i), 1);
+      mbar_init(bar(kRawEmpty + i), kDeqWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kKFull + i), kDeqWarps);
+      mbar_init(bar(kKEmpty + i), 1);
+    }
+    for (int i = 0; i < P::kVStages; ++i) {
+      mbar_init(bar(kVFull + i), kDeqWarps);
+      mbar_init(bar(kVEmpty + i), 1);
+    }
+    for (int i = 0; i < NRT; ++i) {
+      mbar_init(bar(kQFull + i), 4);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(bar(kSFull + 2 * i + j), 1);
+        mbar_init(bar(kPFull + 2 * i + j), 4);
+      }
+      mbar_init(bar(kODone + i), 1);
+    }
+    fence_mbar_init();
+  }
+  if (tid < 8) s_bad[tid] = INT32_MAX;
+  constexpr int kIssueWarp = P::kSoftWarps + kDeqWarps, kLoadWarp = kIssueWarp + 1;
+  if (warp == kIssueWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "n"(P::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+
+  // the line of work: each thread sums its share of the sequences
+  using W = Walk<P::kRows>;
+  const int chunk = (a.n_seqs + P::kThreads - 1) / P::kThreads;
+  const int b_lo = min(tid * chunk, a.n_seqs), b_hi = min(b_lo + chunk, a.n_seqs);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Seq s = seq_at(a, b);
+    mine += W::cost(t, s, W::row_tiles(t, s)) * a.heads;
+    if (blockIdx.x == 0) flag_batch(a, b);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  tc_before();
+  __syncthreads();
+  tc_after();
+  long long total = 0, before = incl - mine;
+  for (int w = 0; w < P::kThreads / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  W walk;
+  // a part spans two steps at least, so that none between a segment's first and last is empty
+  walk.part = max((total + gridDim.x - 1) / gridDim.x, (long long)t.group * 2 * kKeys);
+  walk.cur = (long long)blockIdx.x * walk.part;
+  walk.w1 = min(walk.cur + walk.part, total);
+  if (walk.cur < total && before <= walk.cur && walk.cur < before + mine) {
+    s_base = before;
+    s_b = b_lo;
+  }
+  if (tid == 0) t.ends[blockIdx.x].first = -1;
+  __syncthreads();
+  grid_launch_dependents();
+  walk.base = s_base;
+  walk.b = s_b;
+  const uint32_t tmem = *s_tmem;
+  bool ok = true;
+  Piece p;
+
+  if (warp == kLoadWarp) {
+    // ---------------------------------------------------------------- loader
+    int entry = 0, piece = 0;
+    uint32_t phase = 1;  // the ring starts empty
+    for (; walk.next(a, t, p); ++piece) {
+      const int lim = min(p.sq.len, a.max_pages * a.page_size);
+      const int n32 = 2 * (p.t1 - p.t0);
+      const uint8_t* src = nullptr;
+      for (int i = 0; i < n32; ++i) {
+        if ((i & 31) == 0) {  // lane j looks up the page of the tile i + j
+          const int pos = (2 * p.t0 + i + lane) * kKvTile;
+          int page = 0, pi = 0;
+          if (i + lane < n32 && pos < lim) {
+            pi = kv_page_of(a, pos);
+            page = __ldg(a.table + (size_t)p.b * a.table_stride + pi);
+            if ((unsigned)page >= (unsigned)a.n_pages) {
+              atomicMin(&s_bad[piece & 7], pos);
+              kv_flag(a, MOE_KV_BAD_PAGE);
+              page = 0;  // in bounds; the rows that see it become NaN
+            }
+          }
+          const int in_page = pos < lim ? pos - pi * a.page_size : 0;  // (behind the last key: any tile, nothing of it is seen)
+          src = a.data + (size_t)page * a.page_bytes + (size_t)p.head * a.head_bytes + (size_t)(in_page / kKvTile) * (2 * P::kHalf);
+        }
+        // K of both tiles of a step, then V of both
+        for (int h = 0; h < 2; ++h) {
+          const int from = (i & ~1) + h;  // the tile
+          mbar_wait(bar(kRawEmpty + entry), phase, ok);
+          if (lane == (from & 31)) {
+            mbar_expect_tx(bar(kRawFull + entry), P::kHalf);
+            bulk_g2s(sm + P::kOffRaw + entry * P::kHalf, src + (i & 1) * P::kHalf, P::kHalf, bar(kRawFull + entry));
+          }
+          if (++entry == P::kEntries) entry = 0, phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == kIssueWarp) {
+    // ---------------------------------------------------------------- issue
+    if (lane == 0) {
+      constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
+      uint32_t step = 0;  // over all pieces
+      for (int piece = 0; walk.next(a, t, p); ++piece) {
+        const int n = p.t1 - p.t0;
+        for (int i = 0; i < NRT; ++i) mbar_wait(bar(kQFull + i), piece & 1, ok);
+        for (int j = 0; j <= n; ++j) {
+          const uint32_t g = step + j, kst = g & 1;
+          if (j < n) mbar_wait(bar(kKFull + kst), (g >> 1) & 1, ok);
+          tc_after();
+          for (int i = 0; i < NRT; ++i) {
+            if (j < n) {
+              const uint32_t q = sm + i * P::kQ, k = sm + P::kOffK + kst * P::kStage, d = tmem + (2 * i + kst) * kKeys;
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x)
+                tc_mma(d, desc_k(q + (x >> 2) * (128 * 128) + (x & 3) * 32), desc_k(k + (x >> 2) * (kKeys * 128) + (x & 3) * 32), kIdS,
+                       x > 0);
+              tc_commit(bar(kSFull + 2 * i + kst));
+              if (i == NRT - 1) tc_commit(bar(kKEmpty + kst));
+            }
+            if (j > 0) {
+              const uint32_t f = g - 1, vst = f % P::kVStages, pst = f & 1;
+              mbar_wait(bar(kPFull + 2 * i + pst), (f >> 1) & 1, ok);
+              if (i == 0) mbar_wait(bar(kVFull + vst), (f / P::kVStages) & 1, ok);
+              tc_after();
+              const uint32_t v = sm + P::kOffV + vst * P::kStage, s = tmem + (2 * i + pst) * kKeys, o = tmem + P::kTmemO + i * D;
+#pragma unroll
+              for (int x = 0; x < kKeys / 16; ++x)
+                tc_mma_ts(o, s + x * 8, desc_mn(v + x * 2048, kKeys * 128), kIdO, j > 1 || x > 0);
+              tc_commit(bar(kODone + i));
+              if (i == NRT - 1) tc_commit(bar(kVEmpty + vst));
+            }
+          }
+        }
+        step += n;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= P::kSoftWarps) {
+    // ---------------------------------------------------------------- dequantise
+    const int dt = tid - 32 * P::kSoftWarps;
+    uint32_t magic = 0x64006400u;
+    asm volatile("" : "+r"(magic));
+    int entry = 0;
+    uint32_t phase = 0, step = 0;
+    for (int piece = 0; walk.next(a, t, p); ++piece) {
+      if (dt == 0) s_bad[(piece + 4) & 7] = INT32_MAX;  // (no warp is more than two pieces from another)
+      const int lim = min(p.sq.len, a.max_pages * a.page_size);
+      for (int j = p.t0; j < p.t1; ++j, ++step) {
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t stages = v ? P::kVStages : 2, st = step % stages;
+          const uint32_t empty = v ? bar(kVEmpty + st) : bar(kKEmpty + st), full = v ? bar(kVFull + st) : bar(kKFull + st);
+          mbar_wait(empty, ((step / stages) & 1) ^ 1, ok);
+          for (int h = 0; h < 2; ++h) {
+            const int pos0 = j * kKeys + h * kKvTile;
+            mbar_wait(bar(kRawFull + entry), phase, ok);
+            dequantise_half<D, BITS>(sm + P::kOffRaw + entry * P::kHalf, sm + (v ? P::kOffV : P::kOffK) + st * P::kStage, h * kKvTile,
+                                     dt, v, lim - pos0, pos0, &s_bad[piece & 7], magic);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kRawEmpty + entry));
+            if (++entry == P::kEntries) entry = 0, phase ^= 1;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int i = warp >> 2, row = tid & 127;  // row tile, row in it
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t t_o = tmem + P::kTmemO + i * D + lanes;
+    uint32_t step = 0;
+    for (int piece = 0; walk.next(a, t, p); ++piece) {
+      const int fr = p.rt * P::kRows + i * 128 + row, tok = fr / t.group, gh = fr - tok * t.group;
+      const bool live = fr < p.sq.n * t.group;
+      const int see = live ? p.sq.len - p.sq.n + tok : -1;  // the last position that the row sees
+      const int64_t q_row = p.sq.row0 + tok, q_head = p.head * t.group + gh;
+      float c;
+      {  // queries, scaled by a power of two
+        const uint4* src = reinterpret_cast<const uint4*>(t.q + q_row * t.q_ts + q_head * t.q_hs);
+        float big = 0.f;
+        if (live) {
+#pragma unroll 4
+          for (int x = 0; x < D / 8; ++x) {
+            const uint4 w = src[x];
+            float f[8];
+            unpack2<BF16>(w.x, f[0], f[1]), unpack2<BF16>(w.y, f[2], f[3]), unpack2<BF16>(w.z, f[4], f[5]), unpack2<BF16>(w.w, f[6], f[7]);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) big = fmaxf(big, fabsf(f[y]));
+          }
+        }
+        const int e = row_exponent(big);
+        const float down = query_factor(t.scale_log2, e);
+        c = score_factor(t.scale_log2, e);
+        const uint32_t dst = sm + i * P::kQ + row * 128;
+#pragma unroll 4
+        for (int x = 0; x < D / 8; ++x) {
+          const uint4 w = live ? src[x] : make_uint4(0, 0, 0, 0);
+          float f[8];
+          unpack2<BF16>(w.x, f[0], f[1]), unpack2<BF16>(w.y, f[2], f[3]), unpack2<BF16>(w.z, f[4], f[5]), unpack2<BF16>(w.w, f[6], f[7]);
+          uint32_t h[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            h[y] = BITS == 8 ? pack2<false>(f[2 * y] * down, f[2 * y + 1] * down) : pack2<false>(f[y] * down, f[y + 4] * down);
+          sts128(dst + (x >> 3) * (128 * 128) + (((x & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQFull + i));
+      }
+      // no key is hidden from any row of the warp before this step
+      const int first_row = p.rt * P::kRows + i * 128 + (warp & 3) * 32;
+      const int see_all = p.sq.len - p.sq.n + first_row / t.group;
+      float m = -INFINITY, l = 0.f;
+      for (int j = p.t0; j < p.t1; ++j, ++step) {
+        const uint32_t pst = step & 1, t_s = tmem + (2 * i + pst) * kKeys + lanes;
+        mbar_wait(bar(kSFull + 2 * i + pst), (step >> 1) & 1, ok);
+        tc_after();
+        uint32_t s[2][32];
+        tc_ld32(t_s, s[0]);
+        tc_ld32(t_s + 32, s[1]);
+        tc_wait_ld();
+        const int key0 = j * kKeys;
+        if (key0 + kKeys - 1 > see_all) {
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x)
+            if (key0 + x > see) s[x >> 5][x & 31] = 0xFF800000u;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kKeys; ++x) top = fmaxf(top, __uint_as_float(s[x >> 5][x & 31]));
+        top *= c;
+        const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float r = grow ? ex2(m - top) : 1.f;
+          if (grow) m = top;
+          l *= r;
+          if (j > p.t0) {  // O holds the steps before this one
+            mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
+            tc_after();
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+              uint32_t o[32];
+              tc_ld32(t_o + x, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * r);
+              tc_st32(t_o + x, o);
+            }
+          }
+        }
+        const float z = kPShift - (m == -INFINITY ? 0.f : m);
+        uint32_t ph[32];
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < kKeys; x += 2) {
+          const float e0 = ex2(fmaf(__uint_as_float(s[x >> 5][x & 31]), c, z));
+          const float e1 = ex2(fmaf(__uint_as_float(s[x >> 5][(x & 31) + 1]), c, z));
+          l4[(x >> 1) & 3] += e0 + e1;
+          ph[x >> 1] = pack2<false>(e0, e1);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        // the previous step's product is done by now; seeing each one keeps the barrier's phase known
+        if (step > 0) mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
+        tc_st32(t_s, ph);
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + 2 * i + pst));
+      }
+      mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
+      tc_after();
+      const int bad = *(volatile int*)&s_bad[piece & 7];
+      if (bad <= see || (p.sq.over && see >= a.max_pages * a.page_size)) l = __uint_as_float(kNaN);
+      if (!ok) {
+        if (lane == 0) kv_flag(a, MOE_KV_TIMEOUT);
+        l = __uint_as_float(kNaN);
+      }
+      const bool whole = p.t0 == 0 && p.t1 == p.steps;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const size_t at = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * P::kRows + i * 128 + row;
+      uint16_t* dst = t.out + q_row * t.o_ts + q_head * t.o_hs;
+#pragma unroll 1
+      for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        tc_ld32(t_o + x, o);
+        tc_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 8) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[BITS == 8 ? k : (k & 1) * 4 + (k >> 1)] = __uint_as_float(o[y + k]);
+            if (whole) {
+              *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(pack2<BF16>(f[0] * inv, f[1] * inv), pack2<BF16>(f[2] * inv, f[3] * inv),
+                                                                  pack2<BF16>(f[4] * inv, f[5] * inv), pack2<BF16>(f[6] * inv, f[7] * inv));
+            } else {
+              float4* d4 = reinterpret_cast<float4*>(t.partial + at * D + x + y);
+              d4[0] = make_float4(f[0], f[1], f[2], f[3]);
+              d4[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (live) {
+        if (!whole)
+          t.stats[at] = make_float2(m, l);
+        else if (t.lse)
+          t.lse[q_row * t.nq + q_head] = lse_of(m, l);
+      }
+      if (tid == 0 && p.t0 > 0 && p.t1 == p.steps) t.ends[blockIdx.x] = SegmentEnd{p.first_part, p.b, p.head, p.rt};
+      tc_before();  // O and S have been read before the next piece's products, which wait for its queries or P
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == kIssueWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(P::kTmemCols));
+}
+
+template <int D, int BITS, bool BF16>
+moe_status_t launch_tiles_kernel(const KvArgs& kv, const AttArgs& t, cudaStream_t st) {
+  using P = TilesPlan<D, BITS>;
+  if (!raise_smem(attend_tiles_kernel<D, BITS, BF16>, P::kSmem)) return MOE_ERR_CUDA;
+  attend_tiles_kernel<D, BITS, BF16><<<t.parts, P::kThreads, P::kSmem, st>>>(kv, t);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int BITS>
+moe_status_t launch_tiles(const KvArgs& kv, const AttArgs& t, int dim, bool bf16, cudaStream_t st) {
+  if (dim == 64) return bf16 ? launch_tiles_kernel<64, BITS, true>(kv, t, st) : launch_tiles_kernel<64, BITS, false>(kv, t, st);
+  if (dim == 128) return bf16 ? launch_tiles_kernel<128, BITS, true>(kv, t, st) : launch_tiles_kernel<128, BITS, false>(kv, t, st);
+  return bf16 ? launch_tiles_kernel<256, BITS, true>(kv, t, st) : launch_tiles_kernel<256, BITS, false>(kv, t, st);
+}
+
+}  // namespace
+}  // namespace moe

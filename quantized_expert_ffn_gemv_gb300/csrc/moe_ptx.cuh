@@ -27,13 +27,23 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait: every try suspends for a hardware-chosen time of up to some
-// microseconds, so the limit is reached only after seconds.
-constexpr int kWaitTries = 1 << 22;
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < kWaitTries; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait: ok becomes false after two seconds; a wait that finds it false does not wait.
+constexpr uint64_t kWaitNs = 2000000000ull;
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
+  const uint64_t start = now_ns();
+  do {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+  } while (now_ns() - start < kWaitNs);
   return false;
+}
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool& ok) {
+  if (!mbar_try_wait(bar, parity) && ok) ok = mbar_wait_slow(bar, parity);
 }
 __device__ __forceinline__ void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
 // Orders this thread's ordinary shared-memory accesses before later
