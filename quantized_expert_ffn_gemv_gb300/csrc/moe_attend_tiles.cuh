@@ -67,19 +67,23 @@ struct TilesPlan {
 
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The whole warp calls these with the same operands and one lane issues: under
+// a branch of one lane the operands' way into uniform registers costs more
+// than the product does.
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+  asm volatile("{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
                "l"(a), "l"(b), "r"(idesc), "r"(acc)
                : "memory");
 }
 // A from tensor memory: two fp16 of a row in each 32-bit column.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+  asm volatile("{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
                "r"(a), "l"(b), "r"(idesc), "r"(acc)
                : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     }
   } else if (warp == kIssueWarp) {
     // ---------------------------------------------------------------- issue
-    if (lane == 0) {
+    {
       constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
       uint32_t step = 0;  // over all pieces
       for (int piece = 0; walk.next(a, t, p); ++piece) {
@@ -395,7 +399,6 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
         step += n;
       }
     }
-    __syncwarp();
   } else if (warp >= P::kSoftWarps) {
     // ---------------------------------------------------------------- dequantise
     const int dt = tid - 32 * P::kSoftWarps;
