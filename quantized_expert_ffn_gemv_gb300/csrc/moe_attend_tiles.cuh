@@ -3,10 +3,10 @@
 // A CTA holds NRT row tiles of 128 rows (new token, query head of the kv
 // head's group) and walks the keys 64 at a time:
 //   loader (1 warp)     bulk copies of the pool's half tiles (32 keys' K or V
-//                       with their scales) into a ring
-//   dequantise (4)      integer times scale, rounded to fp16 once, into
-//                       128-byte swizzled stages: K as the K-major and V, which
-//                       has the same rows, as the MN-major operand
+//                       with their scales) into two rings
+//   dequantise (4 + 4)  integer times scale, rounded to fp16 once, into
+//                       128-byte swizzled stages: four warps K as the K-major,
+//                       four V, which has the same rows, as the MN-major operand
 //   issue (1)           S = Q K^T (tcgen05.mma, fp32 in tensor memory, two
 //                       buffers a row tile), O += P V with P read from tensor memory
 //   softmax (4 a tile)  a thread a row: maximum, exponentials, sum; P goes
@@ -14,6 +14,7 @@
 //                       attend_rows_kernel).  O is rescaled in tensor memory
 //                       only when a maximum grew by more than 2^7 since the
 //                       last time, which keeps P below fp16's largest.
+// Registers move from the dequantising warps to the softmax (setmaxnreg).
 // The two row tiles share the dequantised keys and keep the tensor core busy
 // while the other's softmax runs.  Per 64 keys (heads of 128) the tensor core
 // needs about 1,000 cycles, the four schedulers 300 issue slots for the
@@ -38,27 +39,33 @@ using namespace ptx;
 constexpr int kKeys = 64;           // keys of a step
 constexpr int kSegmentKeys = 512;   // what a segment costs beside its keys, in keys
 constexpr float kGrow = 7.f;        // log2 by which a maximum may outgrow its reference
-constexpr int kDeqWarps = 4;
+constexpr int kDeqWarps = 4;        // of either stream
 
 template <int D, int BITS>
 struct TilesPlan {
   static constexpr int NRT = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * NRT;
   static constexpr int kHalf = kv_half_bytes(D, BITS);
-  static constexpr int kEntries = D == 256 ? (BITS == 8 ? 6 : 8) : 12;  // half tiles in the raw ring
+  static constexpr int kHalves = D == 256 && BITS == 8 ? 1 : 2;  // half tiles of a ring entry
+  static constexpr int kEntry = kHalves * kHalf;
+  static constexpr int kEntries = 3;                              // of either ring
   static constexpr int kStage = kKeys * D * 2;
   static constexpr int kVStages = D == 256 ? 1 : 2;
   static constexpr int kQ = 128 * D * 2;
   static constexpr int kOffK = NRT * kQ;
   static constexpr int kOffV = kOffK + 2 * kStage;
   static constexpr int kOffRaw = kOffV + kVStages * kStage;
-  static constexpr int kOffBar = (kOffRaw + kEntries * kHalf + 15) & ~15;
-  // barriers: raw full and empty, K full and empty, V full and empty, Q full, S full, P full, O done
-  static constexpr int kBars = 2 * kEntries + 4 + 2 * kVStages + NRT * 6;
+  static constexpr int kOffBar = (kOffRaw + 2 * kEntries * kEntry + 15) & ~15;
+  // barriers: raw full and empty of either ring, K full and empty, V full and empty, Q full, S full, P full, O done
+  static constexpr int kBars = 4 * kEntries + 4 + 2 * kVStages + NRT * 6;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64;
   static constexpr int kSoftWarps = 4 * NRT;
-  static constexpr int kThreads = 32 * (kSoftWarps + kDeqWarps + 2);
+  static constexpr int kThreads = 32 * (kSoftWarps + 2 * kDeqWarps + 4);
+  // registers of the roles' warpgroups: together no more than the launch's
+  static constexpr int kLaunchRegs = NRT == 2 ? 96 : 128;
+  static constexpr int kSoftRegs = NRT == 2 ? 152 : 208, kDeqRegs = NRT == 2 ? 64 : 104, kRestRegs = NRT == 2 ? 48 : 96;
+  static_assert(kSoftWarps * kSoftRegs + 2 * kDeqWarps * kDeqRegs + 4 * kRestRegs <= kThreads / 32 * kLaunchRegs, "registers");
   static constexpr int kTmemO = NRT * 2 * kKeys;  // S buffers first, then O
   static constexpr int kTmemCols = kTmemO + NRT * D <= 256 ? 256 : 512;
   static_assert(kSmem <= 232448, "shared memory of an SM");
@@ -188,50 +195,76 @@ struct Walk {
   }
 };
 
-// 32 keys' integers times scales into rows key_base .. of a stage.  V: keys
-// from lim on (within the half) are seen by no row and become 0, and so do
-// blocks of non-finite scale; the first such key's position goes to `bad`.
-template <int D, int BITS>
-__device__ __forceinline__ void dequantise_half(uint32_t raw, uint32_t stage, int key_base, int tid, bool is_v, int lim, int pos0,
-                                                int* bad, uint32_t magic) {
+// The integers times scales of an entry's HALVES * 32 keys into rows key_base
+// .. of a stage, all loads first.  V: keys from lim on (of the first key) are
+// seen by no row and become 0, and so do blocks of non-finite scale; the
+// first such key's position goes to `bad`.
+template <int D, int BITS, int HALVES>
+__device__ __forceinline__ void dequantise(uint32_t raw, uint32_t stage, int key_base, int tid, bool is_v, int lim, int pos0, int* bad,
+                                           uint32_t magic) {
   constexpr int R = kv_row_bytes(D, BITS), UPR = R / 16, EPU = 128 / BITS;  // 16-byte units a row, elements a unit
-  const int key = tid & 31, row = key_base + key, turn = kv_turn(key) & (UPR - 1);
+  constexpr int N = (UPR + kDeqWarps - 1) / kDeqWarps;                      // units a thread and half
+  const int key = tid & 31, turn = kv_turn(key) & (UPR - 1);
+  uint4 w4[HALVES][N];
+  uint32_t s2[HALVES][N];
 #pragma unroll
-  for (int c0 = 0; c0 < UPR; c0 += kDeqWarps) {
-    const int c = c0 + (tid >> 5);
-    if (UPR % kDeqWarps && c >= UPR) break;
-    const uint4 w4 = lds128(raw + key * R + ((c ^ turn) << 4));
-    uint32_t sc = lds16(raw + kKvTile * R + ((c * EPU / 32) * kKvTile + key) * 2);
-    if (is_v) {
-      if (key >= lim) {
-        sc = 0;
-      } else if ((sc & 0x7C00u) == 0x7C00u) {
-        sc = 0;
-        atomicMin(bad, pos0 + key);
-      }
+  for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = n * kDeqWarps + (tid >> 5);
+      if (UPR < kDeqWarps && c >= UPR) break;
+      const uint32_t at = raw + h * kv_half_bytes(D, BITS);
+      w4[h][n] = lds128(at + key * R + ((c ^ turn) << 4));
+      s2[h][n] = lds16(at + kKvTile * R + ((c * EPU / 32) * kKvTile + key) * 2);
     }
-    const uint32_t s2 = prmt(sc, sc, 0x1010);
-    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-    for (int i = 0; i < EPU / 8; ++i) {
-      uint32_t h[4];
-      if (BITS == 8) {
+  for (int h = 0; h < HALVES; ++h) {
+    const int k = h * 32 + key, row = key_base + k;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          h[2 * j] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5150), 0x64806480u), s2);
-          h[2 * j + 1] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5352), 0x64806480u), s2);
+    for (int n = 0; n < N; ++n) {
+      const int c = n * kDeqWarps + (tid >> 5);
+      if (UPR < kDeqWarps && c >= UPR) break;
+      uint32_t sc = s2[h][n];
+      if (is_v) {
+        if (k >= lim) {
+          sc = 0;
+        } else if ((sc & 0x7C00u) == 0x7C00u) {
+          sc = 0;
+          atomicMin(bad, pos0 + k);
         }
-      } else {
-        const uint32_t v = w[i], v8 = v >> 8;
-        h[0] = hmul2(hsub2(and_or<0x000F000Fu>(v, magic), 0x64086408u), s2);
-        h[1] = hmul2(hfma2(and_or<0x00F000F0u>(v, magic), 0x2C002C00u, 0xD480D480u), s2);
-        h[2] = hmul2(hsub2(and_or<0x000F000Fu>(v8, magic), 0x64086408u), s2);
-        h[3] = hmul2(hfma2(and_or<0x00F000F0u>(v8, magic), 0x2C002C00u, 0xD480D480u), s2);
       }
-      const int oc = c * (EPU / 8) + i;  // chunk of 8 elements
-      sts128(stage + (oc >> 3) * (kKeys * 128) + row * 128 + (((oc & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+      sc = prmt(sc, sc, 0x1010);
+      const uint32_t w[4] = {w4[h][n].x, w4[h][n].y, w4[h][n].z, w4[h][n].w};
+#pragma unroll
+      for (int i = 0; i < EPU / 8; ++i) {
+        uint32_t x[4];
+        if (BITS == 8) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            x[2 * j] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5150), 0x64806480u), sc);
+            x[2 * j + 1] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5352), 0x64806480u), sc);
+          }
+        } else {
+          const uint32_t v = w[i], v8 = v >> 8;
+          x[0] = hmul2(hsub2(and_or<0x000F000Fu>(v, magic), 0x64086408u), sc);
+          x[1] = hmul2(hfma2(and_or<0x00F000F0u>(v, magic), 0x2C002C00u, 0xD480D480u), sc);
+          x[2] = hmul2(hsub2(and_or<0x000F000Fu>(v8, magic), 0x64086408u), sc);
+          x[3] = hmul2(hfma2(and_or<0x00F000F0u>(v8, magic), 0x2C002C00u, 0xD480D480u), sc);
+        }
+        const int oc = c * (EPU / 8) + i;  // chunk of 8 elements
+        sts128(stage + (oc >> 3) * (kKeys * 128) + row * 128 + (((oc & 7) ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
+      }
     }
   }
+}
+
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int D, int BITS, bool BF16>
@@ -240,19 +273,20 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
   constexpr int NRT = P::NRT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sm = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [&](int i) { return sm + P::kOffBar + 8 * i; };
-  constexpr int kRawFull = 0, kRawEmpty = P::kEntries, kKFull = 2 * P::kEntries, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
+  constexpr int kRawFull = 0, kRawEmpty = 2 * P::kEntries, kKFull = 4 * P::kEntries,  // raw: K's ring, then V's
+                kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
                 kVEmpty = kVFull + P::kVStages, kQFull = kVEmpty + P::kVStages, kSFull = kQFull + NRT, kPFull = kSFull + 2 * NRT,
                 kODone = kPFull + 2 * NRT;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P::kOffMisc);
   int* s_bad = reinterpret_cast<int*>(smem + P::kOffMisc + 16);  // [8], by piece: position of the first bad page or non-finite V
-  __shared__ long long s_sum[16];
+  __shared__ long long s_sum[P::kThreads / 32];
   __shared__ long long s_base;
   __shared__ int s_b;
 
   if (tid == 0) {
-    for (int i = 0; i < P::kEntries; ++i) {
+    for (int i = 0; i < 2 * P::kEntries; ++i) {
       mbar_init(bar(kRawFull + i), 1);
       mbar_init(bar(kRawEmpty + i), kDeqWarps);
     }
@@ -275,7 +309,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     fence_mbar_init();
   }
   if (tid < 8) s_bad[tid] = INT32_MAX;
-  constexpr int kIssueWarp = P::kSoftWarps + kDeqWarps, kLoadWarp = kIssueWarp + 1;
+  constexpr int kIssueWarp = P::kSoftWarps + 2 * kDeqWarps, kLoadWarp = kIssueWarp + 1;
   if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "n"(P::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -324,114 +358,119 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
   bool ok = true;
   Piece p;
 
-  if (warp == kLoadWarp) {
-    // ---------------------------------------------------------------- loader
-    int entry = 0, piece = 0;
-    uint32_t phase = 1;  // the ring starts empty
-    for (; walk.next(a, t, p); ++piece) {
-      const int lim = min(p.sq.len, a.max_pages * a.page_size);
-      const int n32 = 2 * (p.t1 - p.t0);
-      const uint8_t* src = nullptr;
-      for (int i = 0; i < n32; ++i) {
-        if ((i & 31) == 0) {  // lane j looks up the page of the tile i + j
-          const int pos = (2 * p.t0 + i + lane) * kKvTile;
-          int page = 0, pi = 0;
-          if (i + lane < n32 && pos < lim) {
-            pi = kv_page_of(a, pos);
-            page = __ldg(a.table + (size_t)p.b * a.table_stride + pi);
-            if ((unsigned)page >= (unsigned)a.n_pages) {
-              atomicMin(&s_bad[piece & 7], pos);
-              kv_flag(a, MOE_KV_BAD_PAGE);
-              page = 0;  // in bounds; the rows that see it become NaN
+  if (warp >= kIssueWarp) {
+    give_registers<P::kRestRegs>();
+    if (warp == kLoadWarp) {
+      // ---------------------------------------------------------------- loader
+      int entry = 0, piece = 0;
+      uint32_t phase = 1;  // the ring starts empty
+      for (; walk.next(a, t, p); ++piece) {
+        const int lim = min(p.sq.len, a.max_pages * a.page_size);
+        const int n32 = 2 * (p.t1 - p.t0);
+        const uint8_t* src = nullptr;
+        for (int i = 0; i < n32; ++i) {
+          if ((i & 31) == 0) {  // lane j looks up the page of the tile i + j
+            const int pos = (2 * p.t0 + i + lane) * kKvTile;
+            int page = 0, pi = 0;
+            if (i + lane < n32 && pos < lim) {
+              pi = kv_page_of(a, pos);
+              page = __ldg(a.table + (size_t)p.b * a.table_stride + pi);
+              if ((unsigned)page >= (unsigned)a.n_pages) {
+                atomicMin(&s_bad[piece & 7], pos);
+                kv_flag(a, MOE_KV_BAD_PAGE);
+                page = 0;  // in bounds; the rows that see it become NaN
+              }
             }
+            const int in_page = pos < lim ? pos - pi * a.page_size : 0;  // (behind the last key: any tile, nothing of it is seen)
+            src = a.data + (size_t)page * a.page_bytes + (size_t)p.head * a.head_bytes + (size_t)(in_page / kKvTile) * (2 * P::kHalf);
           }
-          const int in_page = pos < lim ? pos - pi * a.page_size : 0;  // (behind the last key: any tile, nothing of it is seen)
-          src = a.data + (size_t)page * a.page_bytes + (size_t)p.head * a.head_bytes + (size_t)(in_page / kKvTile) * (2 * P::kHalf);
-        }
-        // K of both tiles of a step, then V of both
-        for (int h = 0; h < 2; ++h) {
-          const int from = (i & ~1) + h;  // the tile
-          mbar_wait(bar(kRawEmpty + entry), phase, ok);
-          if (lane == (from & 31)) {
-            mbar_expect_tx(bar(kRawFull + entry), P::kHalf);
-            bulk_g2s(sm + P::kOffRaw + entry * P::kHalf, src + (i & 1) * P::kHalf, P::kHalf, bar(kRawFull + entry));
+          // the tiles of an entry, K then V; the lane that looked a tile up copies it
+          if (i % P::kHalves) continue;
+          for (int v = 0; v < 2; ++v) {
+            const int e = v * P::kEntries + entry;
+            mbar_wait(bar(kRawEmpty + e), phase, ok);
+            if (lane == 0) mbar_expect_tx(bar(kRawFull + e), P::kEntry);
+            __syncwarp();
+            if (lane >= (i & 31) && lane < (i & 31) + P::kHalves)
+              bulk_g2s(sm + P::kOffRaw + e * P::kEntry + (lane - (i & 31)) * P::kHalf, src + v * P::kHalf, P::kHalf, bar(kRawFull + e));
           }
           if (++entry == P::kEntries) entry = 0, phase ^= 1;
         }
       }
-    }
-  } else if (warp == kIssueWarp) {
-    // ---------------------------------------------------------------- issue
-    {
-      constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
-      uint32_t step = 0;  // over all pieces
-      for (int piece = 0; walk.next(a, t, p); ++piece) {
-        const int n = p.t1 - p.t0;
-        for (int i = 0; i < NRT; ++i) mbar_wait(bar(kQFull + i), piece & 1, ok);
-        for (int j = 0; j <= n; ++j) {
-          const uint32_t g = step + j, kst = g & 1;
-          if (j < n) mbar_wait(bar(kKFull + kst), (g >> 1) & 1, ok);
-          tc_after();
-          for (int i = 0; i < NRT; ++i) {
-            if (j < n) {
-              const uint32_t q = sm + i * P::kQ, k = sm + P::kOffK + kst * P::kStage, d = tmem + (2 * i + kst) * kKeys;
-#pragma unroll
-              for (int x = 0; x < D / 16; ++x)
-                tc_mma(d, desc_k(q + (x >> 2) * (128 * 128) + (x & 3) * 32), desc_k(k + (x >> 2) * (kKeys * 128) + (x & 3) * 32), kIdS,
-                       x > 0);
-              tc_commit(bar(kSFull + 2 * i + kst));
-              if (i == NRT - 1) tc_commit(bar(kKEmpty + kst));
-            }
-            if (j > 0) {
-              const uint32_t f = g - 1, vst = f % P::kVStages, pst = f & 1;
-              mbar_wait(bar(kPFull + 2 * i + pst), (f >> 1) & 1, ok);
-              if (i == 0) mbar_wait(bar(kVFull + vst), (f / P::kVStages) & 1, ok);
-              tc_after();
-              const uint32_t v = sm + P::kOffV + vst * P::kStage, s = tmem + (2 * i + pst) * kKeys, o = tmem + P::kTmemO + i * D;
-#pragma unroll
-              for (int x = 0; x < kKeys / 16; ++x)
-                tc_mma_ts(o, s + x * 8, desc_mn(v + x * 2048, kKeys * 128), kIdO, j > 1 || x > 0);
-              tc_commit(bar(kODone + i));
-              if (i == NRT - 1) tc_commit(bar(kVEmpty + vst));
+    } else if (warp == kIssueWarp) {
+      // ---------------------------------------------------------------- issue
+      {
+        constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
+        uint32_t step = 0;  // over all pieces
+        for (int piece = 0; walk.next(a, t, p); ++piece) {
+          const int n = p.t1 - p.t0;
+          for (int i = 0; i < NRT; ++i) mbar_wait(bar(kQFull + i), piece & 1, ok);
+          for (int j = 0; j <= n; ++j) {
+            const uint32_t g = step + j, kst = g & 1;
+            if (j < n) mbar_wait(bar(kKFull + kst), (g >> 1) & 1, ok);
+            tc_after();
+            for (int i = 0; i < NRT; ++i) {
+              if (j < n) {
+                const uint32_t q = sm + i * P::kQ, k = sm + P::kOffK + kst * P::kStage, d = tmem + (2 * i + kst) * kKeys;
+  #pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                  tc_mma(d, desc_k(q + (x >> 2) * (128 * 128) + (x & 3) * 32), desc_k(k + (x >> 2) * (kKeys * 128) + (x & 3) * 32), kIdS,
+                         x > 0);
+                tc_commit(bar(kSFull + 2 * i + kst));
+                if (i == NRT - 1) tc_commit(bar(kKEmpty + kst));
+              }
+              if (j > 0) {
+                const uint32_t f = g - 1, vst = f % P::kVStages, pst = f & 1;
+                mbar_wait(bar(kPFull + 2 * i + pst), (f >> 1) & 1, ok);
+                if (i == 0) mbar_wait(bar(kVFull + vst), (f / P::kVStages) & 1, ok);
+                tc_after();
+                const uint32_t v = sm + P::kOffV + vst * P::kStage, s = tmem + (2 * i + pst) * kKeys, o = tmem + P::kTmemO + i * D;
+  #pragma unroll
+                for (int x = 0; x < kKeys / 16; ++x)
+                  tc_mma_ts(o, s + x * 8, desc_mn(v + x * 2048, kKeys * 128), kIdO, j > 1 || x > 0);
+                tc_commit(bar(kODone + i));
+                if (i == NRT - 1) tc_commit(bar(kVEmpty + vst));
+              }
             }
           }
+          step += n;
         }
-        step += n;
       }
     }
   } else if (warp >= P::kSoftWarps) {
     // ---------------------------------------------------------------- dequantise
-    const int dt = tid - 32 * P::kSoftWarps;
+    give_registers<P::kDeqRegs>();
+    const int dt = tid & 127;
+    const bool v = warp >= P::kSoftWarps + kDeqWarps;  // which stream
+    const uint32_t stages = v ? P::kVStages : 2;
     uint32_t magic = 0x64006400u;
     asm volatile("" : "+r"(magic));
     int entry = 0;
     uint32_t phase = 0, step = 0;
     for (int piece = 0; walk.next(a, t, p); ++piece) {
-      if (dt == 0) s_bad[(piece + 4) & 7] = INT32_MAX;  // (no warp is more than two pieces from another)
+      if (v && dt == 0) s_bad[(piece + 4) & 7] = INT32_MAX;  // (no warp is more than three pieces from another)
       const int lim = min(p.sq.len, a.max_pages * a.page_size);
       for (int j = p.t0; j < p.t1; ++j, ++step) {
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t stages = v ? P::kVStages : 2, st = step % stages;
-          const uint32_t empty = v ? bar(kVEmpty + st) : bar(kKEmpty + st), full = v ? bar(kVFull + st) : bar(kKFull + st);
-          mbar_wait(empty, ((step / stages) & 1) ^ 1, ok);
-          for (int h = 0; h < 2; ++h) {
-            const int pos0 = j * kKeys + h * kKvTile;
-            mbar_wait(bar(kRawFull + entry), phase, ok);
-            dequantise_half<D, BITS>(sm + P::kOffRaw + entry * P::kHalf, sm + (v ? P::kOffV : P::kOffK) + st * P::kStage, h * kKvTile,
-                                     dt, v, lim - pos0, pos0, &s_bad[piece & 7], magic);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kRawEmpty + entry));
-            if (++entry == P::kEntries) entry = 0, phase ^= 1;
-          }
-          fence_async_shared();
+        const uint32_t st = step % stages;
+        mbar_wait(v ? bar(kVEmpty + st) : bar(kKEmpty + st), ((step / stages) & 1) ^ 1, ok);
+#pragma unroll
+        for (int h = 0; h < 2; h += P::kHalves) {
+          const int pos0 = j * kKeys + h * kKvTile, e = (v ? P::kEntries : 0) + entry;
+          mbar_wait(bar(kRawFull + e), phase, ok);
+          dequantise<D, BITS, P::kHalves>(sm + P::kOffRaw + e * P::kEntry, sm + (v ? P::kOffV : P::kOffK) + st * P::kStage, h * kKvTile, dt,
+                                          v, lim - pos0, pos0, &s_bad[piece & 7], magic);
           __syncwarp();
-          if (lane == 0) mbar_arrive(full);
+          if (lane == 0) mbar_arrive(bar(kRawEmpty + e));
+          if (++entry == P::kEntries) entry = 0, phase ^= 1;
         }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v ? bar(kVFull + st) : bar(kKFull + st));
       }
     }
   } else {
     // ---------------------------------------------------------------- softmax
+    take_registers<P::kSoftRegs>();
     const int i = warp >> 2, row = tid & 127;  // row tile, row in it
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t t_o = tmem + P::kTmemO + i * D + lanes;
@@ -589,8 +628,16 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
 template <int D, int BITS, bool BF16>
 moe_status_t launch_tiles_kernel(const KvArgs& kv, const AttArgs& t, cudaStream_t st) {
   using P = TilesPlan<D, BITS>;
-  if (!raise_smem(attend_tiles_kernel<D, BITS, BF16>, P::kSmem)) return MOE_ERR_CUDA;
-  attend_tiles_kernel<D, BITS, BF16><<<t.parts, P::kThreads, P::kSmem, st>>>(kv, t);
+  const auto kernel = attend_tiles_kernel<D, BITS, BF16>;
+  if (!raise_smem(kernel, P::kSmem)) return MOE_ERR_CUDA;
+  // the roles' registers come out of the launch's: with fewer the softmax would wait for its share for good
+  static int enough = 0;
+  if (!__atomic_load_n(&enough, __ATOMIC_RELAXED)) {
+    cudaFuncAttributes at{};
+    if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess || at.numRegs < P::kLaunchRegs) return MOE_ERR_CUDA;
+    __atomic_store_n(&enough, 1, __ATOMIC_RELAXED);
+  }
+  kernel<<<t.parts, P::kThreads, P::kSmem, st>>>(kv, t);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
