@@ -14,6 +14,7 @@ using namespace ptx;
 // (WARPS 8) a CTA takes one row, its warps every eighth part; many segments
 // have a part or two each: then (WARPS 1) every warp takes a row.
 constexpr int kJoinThreads = 256;
+constexpr int kSharedTiles = 2;  // row tiles from which a shared prefix gets a pass of its own
 
 template <int D, bool BF16, int WARPS>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const KvArgs a, const AttArgs t) {
@@ -94,19 +95,100 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const KvArgs 
   }
 }
 
+// Merges a segment's parts, or its whole, into a row's running result; the warp's lanes hold D / 32 elements each.
+template <int D>
+__device__ __forceinline__ void merge_span(const AttArgs& t, int64_t segment, int row, int lane, float& m, float& l, float (&o)[D / 32]) {
+  constexpr int NE = D / 32, kAhead = 4;
+  const Span s = t.spans[segment];
+  const bool whole = s.first == kWhole;
+  const int c0 = whole ? 0 : s.first, c1 = whole ? 0 : s.last;
+  for (int c = c0; c <= c1; c += kAhead) {
+    float2 st[kAhead];
+    float v[kAhead][NE];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int ck = c + k;
+      st[k] = make_float2(-INFINITY, 0.f);
+      if (ck > c1) continue;
+      const size_t at = (whole ? (size_t)segment : (size_t)ck * 2 + (ck == c0 ? 1 : 0)) * t.tile_rows + row;
+      st[k] = (whole ? t.whole_stats : t.stats)[at];
+      const float* src = (whole ? t.whole : t.partial) + at * D + lane * NE;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[k][i] = src[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (c + k > c1) break;
+      const float n = fmaxf(m, st[k].x);
+      const float wo = m == -INFINITY ? 0.f : ex2(m - n), wn = st[k].x == -INFINITY ? 0.f : ex2(st[k].x - n);
+      l = (l != l ? l : l * wo) + (st[k].y != st[k].y ? st[k].y : st[k].y * wn);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) o[i] = o[i] * wo + v[k][i] * wn;
+      m = n;
+    }
+  }
+}
+
+// A warp a row (token, query head): what it saw of the shared prefix (`pre`) and behind it (`t`).
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const KvArgs a, const AttArgs t, const AttArgs pre) {
+  constexpr int NE = D / 32;
+  grid_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int tok = (int)(r / t.nq), qh = (int)(r - (int64_t)tok * t.nq);
+  if (tok >= a.n_tokens) return;
+  const int b = kv_seq_of(a, tok);
+  if (b < 0) return;
+  const Seq sq = seq_at(a, b);
+  if (tok - sq.row0 >= sq.n) return;
+  const int head = qh / t.group, g = qh - head * t.group;
+  float m = -INFINITY, l = 0.f, o[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) o[i] = 0.f;
+  const int see = sq.len - sq.n + tok - sq.row0;
+  if (see >= 0) {
+    const int n = min(max(__ldg(a.cu + a.n_seqs), 0), a.n_tokens), tiles = (n * t.group + pre.tile_rows - 1) / pre.tile_rows;
+    const int fr = tok * t.group + g, rt = fr / pre.tile_rows;
+    merge_span<D>(pre, (int64_t)head * tiles + rt, fr - rt * pre.tile_rows, lane, m, l, o);
+  }
+  if (min(sq.len, a.max_pages * a.page_size) > t.shared) {
+    const int fr = (tok - sq.row0) * t.group + g, rt = fr / t.tile_rows;
+    merge_span<D>(t, ((int64_t)b * a.heads + head) * t.max_row_tiles + rt, fr - rt * t.tile_rows, lane, m, l, o);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* dst = t.out + (int64_t)tok * t.o_ts + (int64_t)qh * t.o_hs;
+#pragma unroll
+  for (int i = 0; i < NE; i += 2) *reinterpret_cast<uint32_t*>(dst + lane * NE + i) = pack2<BF16>(o[i] * inv, o[i + 1] * inv);
+  if (t.lse && lane == 0) t.lse[(int64_t)tok * t.nq + qh] = lse_of(m, l);
+}
+
+// Where a kernel's results lie in the workspace, from `at` on.
 struct Workspace {
-  size_t partial, stats, ends, bytes;
+  size_t partial, stats, ends, whole, whole_stats, spans, end;
 };
 
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
-Workspace plan_workspace(int parts, int tile_rows, int dim) {
+// segments: those that leave results of their own (with a shared prefix).
+Workspace plan_workspace(size_t at, int parts, int tile_rows, int dim, int64_t segments) {
   Workspace w{};
-  w.partial = 0;
+  w.partial = at;
   w.stats = up16(w.partial + (size_t)parts * 2 * tile_rows * dim * 4);
   w.ends = up16(w.stats + (size_t)parts * 2 * tile_rows * 8);
-  w.bytes = up16(w.ends + (size_t)parts * sizeof(SegmentEnd));
+  w.whole = up16(w.ends + (size_t)parts * sizeof(SegmentEnd));
+  w.whole_stats = up16(w.whole + (size_t)segments * tile_rows * dim * 4);
+  w.spans = up16(w.whole_stats + (size_t)segments * tile_rows * 8);
+  w.end = up16(w.spans + (size_t)segments * sizeof(Span));
   return w;
+}
+void place(AttArgs* t, uint8_t* base, const Workspace& w) {
+  t->partial = (float*)(base + w.partial);
+  t->stats = (float2*)(base + w.stats);
+  t->ends = (SegmentEnd*)(base + w.ends);
+  t->whole = (float*)(base + w.whole);
+  t->whole_stats = (float2*)(base + w.whole_stats);
+  t->spans = (Span*)(base + w.spans);
 }
 
 template <int D, bool BF16>
@@ -133,12 +215,32 @@ moe_status_t launch_join(const KvArgs& kv, const AttArgs& t, bool bf16, cudaStre
   return bf16 ? launch_join_type<D, true>(kv, t, st) : launch_join_type<D, false>(kv, t, st);
 }
 
+template <int D>
+moe_status_t launch_join_shared(const KvArgs& kv, const AttArgs& t, const AttArgs& pre, bool bf16, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  const int64_t rows = (int64_t)kv.n_tokens * t.nq, warps = kJoinThreads / 32;
+  cfg.gridDim = dim3((unsigned)((rows + warps - 1) / warps));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, attend_join_shared_kernel<D, true>, kv, t, pre)
+                             : cudaLaunchKernelEx(&cfg, attend_join_shared_kernel<D, false>, kv, t, pre);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // What both entries derive from their arguments.
 struct AttPlan {
   KvArgs kv;
-  bool tiles;  // attend_tiles_kernel
-  int parts, tile_rows;
-  Workspace ws;
+  bool tiles;   // attend_tiles_kernel
+  int shared;   // keys that are read once for the batch
+  int parts, tile_rows, max_row_tiles;
+  int pre_parts, pre_rows;
+  Workspace ws, pre_ws;
+  size_t bytes;
 };
 
 moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int32_t n_q, int32_t shared_tokens, AttPlan* p) {
@@ -152,17 +254,30 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   st = device_sms(&sms);
   if (st != MOE_OK) return st;
   // A sequence's rows in tiles of 8 while they suffice, then 16 and 32, which
-  // share the dequantised keys and values (heads of 256 have registers for 16);
-  // above 64 rows the tensor cores' tiles of 256 (128 for heads of 256).
-  p->tiles = rows > 64;
-  if (p->tiles) {
-    p->tile_rows = cache->head_dim == 256 ? 128 : 256;
-    p->parts = sms;
-  } else {
-    p->tile_rows = rows <= 8 ? 8 : rows <= 16 || cache->head_dim == 256 ? 16 : 32;
-    p->parts = sms * rows_blocks(cache->head_dim, cache->bits, p->tile_rows);
+  // share the dequantised keys and values.  Above 64 rows the tensor cores'
+  // tiles of 256 (128 for heads of 256); heads of 256, which have registers for
+  // 16 rows on the other path, above 16: 12 sequences of 60,000 to 131,072
+  // tokens at 32 rows take 265 us there and 328 in tiles of 16.  Heads of 128
+  // take 109 and 111 us at 32 rows (32 sequences of 8,192).
+  const int dim = cache->head_dim, heads = cache->n_kv_heads, group = n_q / heads;
+  const int big = dim == 256 ? 128 : 256;
+  p->tiles = rows > (dim == 256 ? 16 : 64);
+  p->tile_rows = p->tiles ? big : rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32;
+  p->parts = p->tiles ? sms : sms * rows_blocks(dim, cache->bits, p->tile_rows);
+  p->max_row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
+  // A prefix is worth a pass of its own when the batch's rows would read it several times over.
+  const int64_t all_rows = (int64_t)batch->n_tokens * group;
+  p->shared = !p->tiles && all_rows > kSharedTiles * p->tile_rows ? shared_tokens : 0;
+  p->pre_parts = sms;
+  p->pre_rows = big;
+  const int64_t segments = (int64_t)batch->n_seqs * heads * p->max_row_tiles, pre_segments = heads * ((all_rows + big - 1) / big);
+  if (segments > INT32_MAX || pre_segments > INT32_MAX || all_rows * heads > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  p->ws = plan_workspace(0, p->parts, p->tile_rows, dim, p->shared ? segments : 0);
+  p->bytes = p->ws.end;
+  if (p->shared) {
+    p->pre_ws = plan_workspace(p->bytes, p->pre_parts, p->pre_rows, dim, pre_segments);
+    p->bytes = p->pre_ws.end;
   }
-  p->ws = plan_workspace(p->parts, p->tile_rows, cache->head_dim);
   return MOE_OK;
 }
 
@@ -181,7 +296,7 @@ extern "C" MOE_API moe_status_t moe_kv_attend_workspace(const moe_kv_cache_t* ca
   *bytes = 0;
   moe::AttPlan p;
   const moe_status_t st = moe::attend_plan(cache, batch, n_q, shared_tokens, &p);
-  if (st == MOE_OK) *bytes = p.ws.bytes;
+  if (st == MOE_OK) *bytes = p.bytes;
   return st;
 }
 
@@ -198,7 +313,7 @@ extern "C" MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const
   const int dim = cache->head_dim;
   if (!moe::heads_ok(q, dim) || !moe::out_heads_ok(out, n_q, p.kv.n_tokens, dim)) return MOE_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 15)) return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < p.ws.bytes) return MOE_ERR_OUT_OF_MEMORY;
+  if (workspace_bytes < p.bytes) return MOE_ERR_OUT_OF_MEMORY;
   uint8_t* w = (uint8_t*)workspace;
   moe::AttArgs t{};
   t.q = (const uint16_t*)q->data;
@@ -213,16 +328,29 @@ extern "C" MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const
   t.group = n_q / cache->n_kv_heads;
   t.tile_rows = p.tile_rows;
   t.parts = p.parts;
-  t.partial = (float*)(w + p.ws.partial);
-  t.stats = (float2*)(w + p.ws.stats);
-  t.ends = (moe::SegmentEnd*)(w + p.ws.ends);
+  t.shared = p.shared;
+  t.max_row_tiles = p.max_row_tiles;
+  moe::place(&t, w, p.ws);
   const bool bf = dtype == MOE_BF16;
   const cudaStream_t s = (cudaStream_t)cuda_stream;
-  const auto launch = p.tiles ? (cache->bits == 8 ? moe::launch_tiles8 : moe::launch_tiles4)
-                              : (cache->bits == 8 ? moe::launch_rows8 : moe::launch_rows4);
-  const moe_status_t main_st = launch(p.kv, t, dim, bf, s);
-  if (main_st != MOE_OK) return main_st;
-  if (dim == 64) return moe::launch_join<64>(p.kv, t, bf, s);
-  if (dim == 128) return moe::launch_join<128>(p.kv, t, bf, s);
-  return moe::launch_join<256>(p.kv, t, bf, s);
+  const bool wide = cache->bits == 8;
+  moe_status_t done;
+  if (!p.shared) {
+    const auto launch = p.tiles ? (wide ? moe::launch_tiles8 : moe::launch_tiles4) : (wide ? moe::launch_rows8 : moe::launch_rows4);
+    done = launch(p.kv, t, dim, bf, s);
+    if (done != MOE_OK) return done;
+    if (dim == 64) return moe::launch_join<64>(p.kv, t, bf, s);
+    if (dim == 128) return moe::launch_join<128>(p.kv, t, bf, s);
+    return moe::launch_join<256>(p.kv, t, bf, s);
+  }
+  moe::AttArgs pre = t;
+  pre.parts = p.pre_parts;
+  pre.tile_rows = p.pre_rows;
+  moe::place(&pre, w, p.pre_ws);
+  done = (wide ? moe::launch_tiles8 : moe::launch_tiles4)(p.kv, pre, dim, bf, s);
+  if (done == MOE_OK) done = (wide ? moe::launch_rows8 : moe::launch_rows4)(p.kv, t, dim, bf, s);
+  if (done != MOE_OK) return done;
+  if (dim == 64) return moe::launch_join_shared<64>(p.kv, t, pre, bf, s);
+  if (dim == 128) return moe::launch_join_shared<128>(p.kv, t, pre, bf, s);
+  return moe::launch_join_shared<256>(p.kv, t, pre, bf, s);
 }

@@ -7,6 +7,12 @@
 // reference maximum, the maximum, the sum): in its slot 1 where it begins at
 // the segment's first tile, in slot 0 otherwise, and the CTA that has the
 // last tile notes the segment in `ends`.  attend_join_kernel merges those.
+//
+// With a shared prefix, attend_tiles_kernel runs over its keys with the rows
+// of all sequences as one, attend_rows_kernel over what is behind it, and
+// attend_join_shared_kernel merges both for every row: then no kernel finishes
+// a segment, whole ones leave their result in `whole`, and every segment's
+// parts are noted in `spans`.
 #pragma once
 
 #include <cfloat>
@@ -26,6 +32,12 @@ struct SegmentEnd {
   int first, b, head, rt;
 };
 
+// The parts of a segment: first .. last, or kWhole for one that a single CTA finished.
+constexpr int kWhole = -2;
+struct Span {
+  int first, last;
+};
+
 struct AttArgs {
   const uint16_t* q;
   int64_t q_ts, q_hs;
@@ -39,6 +51,11 @@ struct AttArgs {
   float* partial;    // [parts][2][tile_rows][D]
   float2* stats;     // [parts][2][tile_rows] (maximum, sum)
   SegmentEnd* ends;  // [parts]
+  int shared;          // keys of the shared prefix, 0 = none; what follows is for it
+  int max_row_tiles;   // row tiles of a sequence at most (attend_rows_kernel's segments)
+  float* whole;        // [segments][tile_rows][D]
+  float2* whole_stats; // [segments][tile_rows]
+  Span* spans;         // [segments]
 };
 
 // A sequence's arrays, made harmless: new tokens that cannot be are none

@@ -197,9 +197,10 @@ __device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint
   }
 }
 
-// 32-token tiles of keys that a sequence's segments have, and its row tiles.
-__device__ __forceinline__ int key_tiles(const KvArgs& a, const Seq& s) {
-  return max(1, (min(s.len, a.max_pages * a.page_size) + kKvTile - 1) / kKvTile);
+// 32-token tiles of keys that a sequence's segments have (behind a shared prefix there may be none), and its row tiles.
+__device__ __forceinline__ int key_tiles(const KvArgs& a, const AttArgs& t, const Seq& s) {
+  const int keys = min(s.len, a.max_pages * a.page_size) - t.shared;
+  return max(t.shared ? 0 : 1, (keys + kKvTile - 1) / kKvTile);
 }
 template <int ROWS>
 __device__ __forceinline__ int row_tiles(const AttArgs& t, const Seq& s) {
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const Seq s = seq_at(a, b);
-    mine += (long long)row_tiles<kRows>(t, s) * a.heads * (key_tiles(a, s) + kSegment);
+    mine += (long long)row_tiles<kRows>(t, s) * a.heads * (key_tiles(a, t, s) + kSegment);
     if (blockIdx.x == 0) flag_batch(a, b);
   }
   long long incl = mine;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
   const int g = lane >> 2, tq = lane & 3;
   while (cur < w1) {
     const Seq sq = seq_at(a, b);
-    const int tiles = key_tiles(a, sq), n_rt = row_tiles<kRows>(t, sq), units = tiles + kSegment;
+    const int tiles = key_tiles(a, t, sq), n_rt = row_tiles<kRows>(t, sq), units = tiles + kSegment;
     const long long size = (long long)n_rt * a.heads * units;
     const long long local = cur - base;
     if (local >= size) {
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
       first = from;
       const int i = from + lane;
       if (i < nt) {
-        const int pos = (t0 + warp + kAttWarps * i) * kKvTile, pi = kv_page_of(a, pos);
+        const int pos = t.shared + (t0 + warp + kAttWarps * i) * kKvTile, pi = kv_page_of(a, pos);
         int page = pi < a.max_pages ? __ldg(a.table + (size_t)b * a.table_stride + pi) : -1;
         if ((unsigned)page >= (unsigned)a.n_pages) {
           if (sq.len > 0) bad_page = true;  // an empty sequence's one tile holds nothing that is seen
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
     const int see_max = sq.len - sq.n + (rt * kRows + rows - 1) / t.group;
 
     for (int i = 0; i < nt; ++i) {
-      const int key0 = (t0 + warp + kAttWarps * i) * kKvTile;
+      const int key0 = t.shared + (t0 + warp + kAttWarps * i) * kKvTile;
       const bool edge = key0 + kKvTile - 1 > see_min;
       float s[2][NT][4];
       {
@@ -523,9 +524,12 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         ll += st.y != st.y ? st.y : st.y * wgt[w];
       }
       const bool whole = t0 == 0 && t1 == tiles;
+      const int64_t segment = ((int64_t)b * a.heads + head) * t.max_row_tiles + rt;  // (with a shared prefix)
       const int fr = rt * kRows + row, tok = fr / t.group, gh = fr - tok * t.group;
       const float inv = ll == 0.f ? 0.f : 1.f / ll;
-      const size_t at = ((size_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * kRows + row;
+      const bool finish = whole && !t.shared;
+      const size_t at = whole ? (size_t)segment * kRows + row : ((size_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * kRows + row;
+      float* partial = whole ? t.whole : t.partial;
       if (row < rows) {
 #pragma unroll
         for (int i = 0; i < NE; i += 4) {
@@ -540,22 +544,25 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
             acc.z = fmaf(wgt[w], v.z, acc.z);
             acc.w = fmaf(wgt[w], v.w, acc.w);
           }
-          if (whole)
+          if (finish)
             *reinterpret_cast<uint2*>(t.out + (int64_t)(sq.row0 + tok) * t.o_ts + (int64_t)(head * t.group + gh) * t.o_hs + d) =
                 make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
           else
-            *reinterpret_cast<float4*>(t.partial + at * D + d) = acc;
+            *reinterpret_cast<float4*>(partial + at * D + d) = acc;
         }
         if (sub == 0) {
-          if (!whole)
-            t.stats[at] = make_float2(mm, ll);
+          if (!finish)
+            (whole ? t.whole_stats : t.stats)[at] = make_float2(mm, ll);
           else if (t.lse)
             t.lse[(int64_t)(sq.row0 + tok) * t.nq + head * t.group + gh] = lse_of(mm, ll);
         }
       }
-      if (t0 > 0 && t1 == tiles && tid == 0) {
-        const long long start = cur - u1;  // the segment's place on the line
-        t.ends[blockIdx.x] = SegmentEnd{(int)((start + kSegment) / part), b, head, rt};
+      if (t1 == tiles && tid == 0) {
+        const int first_part = (int)((cur - u1 + kSegment) / part);  // (cur - u1: the segment's place on the line)
+        if (t.shared)
+          t.spans[segment] = Span{whole ? kWhole : first_part, (int)blockIdx.x};
+        else if (!whole)
+          t.ends[blockIdx.x] = SegmentEnd{first_part, b, head, rt};
       }
     }
   }

@@ -111,6 +111,13 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) 
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -134,25 +141,31 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // A part of a segment: key steps t0 .. t1 of row tile rt.
 struct Piece {
   int b, head, rt, t0, t1, steps;
-  Seq sq;
+  int rows;        // live rows of the row tile
   int first_part;  // the CTA that has step 0
+  int lim;         // keys that hold anything
+  Seq sq;
 };
 
-// The CTA's share of the line of work.
+// The CTA's share of the line of work.  With a shared prefix there is one
+// sequence, `pre`: the new tokens of all, in front of them as many keys as the
+// prefix has (its len), read through the block table's row b.
 template <int ROWS>
 struct Walk {
   long long part, w1, cur, base;
   int b;
+  Seq pre;
 
   // Cost of a head's row tiles 0 .. rt - 1, in keys times the group.
   static __device__ __forceinline__ long long cost(const AttArgs& t, const Seq& s, long long rt) {
+    if (t.shared) return rt * t.group * (kSegmentKeys + (long long)s.len);
     return rt * t.group * (kSegmentKeys + (long long)max(s.len - s.n, 0)) + (long long)ROWS * rt * (rt + 1) / 2;
   }
   static __device__ __forceinline__ int row_tiles(const AttArgs& t, const Seq& s) { return (s.n * t.group + ROWS - 1) / ROWS; }
 
   __device__ bool next(const KvArgs& a, const AttArgs& t, Piece& p) {
     while (cur < w1) {
-      const Seq s = seq_at(a, b);
+      const Seq s = t.shared ? pre : seq_at(a, b);
       const int n_rt = row_tiles(t, s);
       const long long per_head = cost(t, s, n_rt), local = cur - base;
       if (local >= per_head * a.heads) {
@@ -175,7 +188,8 @@ struct Walk {
       cur += x1 - x0;
       // the keys that the tile's last row sees
       const int last = min((lo + 1) * ROWS, s.n * t.group) - 1;
-      const int lim = min(min(s.len - s.n + last / t.group + 1, s.len), a.max_pages * a.page_size);
+      p.lim = min(s.len, a.max_pages * a.page_size);
+      const int lim = t.shared ? p.lim : min(s.len - s.n + last / t.group + 1, p.lim);
       p.steps = max(1, (lim + kKeys - 1) / kKeys);
       auto step_at = [&](long long pos) {
         const long long u = pos / t.group - kSegmentKeys;
@@ -187,6 +201,7 @@ struct Walk {
       p.b = b;
       p.head = head;
       p.rt = lo;
+      p.rows = s.n * t.group - lo * ROWS;
       p.sq = s;
       p.first_part = (int)((seg_start + min((long long)t.group * (kSegmentKeys + 1), all) - 1) / part);
       return true;
@@ -320,10 +335,21 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
   const int chunk = (a.n_seqs + P::kThreads - 1) / P::kThreads;
   const int b_lo = min(tid * chunk, a.n_seqs), b_hi = min(b_lo + chunk, a.n_seqs);
   long long mine = 0;
+  int longest = 0, longest_b = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const Seq s = seq_at(a, b);
     mine += W::cost(t, s, W::row_tiles(t, s)) * a.heads;
+    if (s.len > longest) longest = s.len, longest_b = b;
     if (blockIdx.x == 0) flag_batch(a, b);
+  }
+  __shared__ int s_long[2];
+  if (t.shared) {  // the prefix is read through the longest sequence's row; there are no keys behind that one's length
+    if (tid == 0) s_long[0] = s_long[1] = 0;
+    __syncthreads();
+    atomicMax(&s_long[0], longest);
+    __syncthreads();
+    if (longest > 0 && longest == s_long[0]) s_long[1] = longest_b;  // (any of them)
+    mine = 0;
   }
   long long incl = mine;
 #pragma unroll
@@ -342,10 +368,17 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
   }
   W walk;
   // a part spans two steps at least, so that none between a segment's first and last is empty
+  if (t.shared) {
+    const int n = min(max(__ldg(a.cu + a.n_seqs), 0), a.n_tokens);
+    walk.pre = Seq{0, n, min(t.shared, s_long[0]), false};
+    total = n > 0 && walk.pre.len > 0 ? W::cost(t, walk.pre, W::row_tiles(t, walk.pre)) * a.heads : 0;
+  }
   walk.part = max((total + gridDim.x - 1) / gridDim.x, (long long)t.group * 2 * kKeys);
   walk.cur = (long long)blockIdx.x * walk.part;
   walk.w1 = min(walk.cur + walk.part, total);
-  if (walk.cur < total && before <= walk.cur && walk.cur < before + mine) {
+  if (t.shared) {
+    if (tid == 0) s_base = 0, s_b = s_long[1];
+  } else if (walk.cur < total && before <= walk.cur && walk.cur < before + mine) {
     s_base = before;
     s_b = b_lo;
   }
@@ -365,7 +398,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
       int entry = 0, piece = 0;
       uint32_t phase = 1;  // the ring starts empty
       for (; walk.next(a, t, p); ++piece) {
-        const int lim = min(p.sq.len, a.max_pages * a.page_size);
+        const int lim = p.lim;
         const int n32 = 2 * (p.t1 - p.t0);
         const uint8_t* src = nullptr;
         for (int i = 0; i < n32; ++i) {
@@ -401,39 +434,45 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
       // ---------------------------------------------------------------- issue
       {
         constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
-        uint32_t step = 0;  // over all pieces
-        for (int piece = 0; walk.next(a, t, p); ++piece) {
-          const int n = p.t1 - p.t0;
-          for (int i = 0; i < NRT; ++i) mbar_wait(bar(kQFull + i), piece & 1, ok);
+        uint32_t step = 0, own0 = 0, own1 = 0, pieces0 = 0, pieces1 = 0;  // steps over all pieces; either row tile's steps and pieces
+        while (walk.next(a, t, p)) {
+          const int n = p.t1 - p.t0, tiles = min(NRT, (p.rows + 127) / 128);  // row tiles that hold rows
+          mbar_wait(bar(kQFull), pieces0++ & 1, ok);
+          if (tiles > 1) mbar_wait(bar(kQFull + 1), pieces1++ & 1, ok);
           for (int j = 0; j <= n; ++j) {
             const uint32_t g = step + j, kst = g & 1;
             if (j < n) mbar_wait(bar(kKFull + kst), (g >> 1) & 1, ok);
             tc_after();
-            for (int i = 0; i < NRT; ++i) {
+#pragma unroll 1
+            for (int i = 0; i < tiles; ++i) {  // (unrolled, the operands would not fit the uniform registers)
+              const uint32_t own = i ? own1 : own0;
               if (j < n) {
-                const uint32_t q = sm + i * P::kQ, k = sm + P::kOffK + kst * P::kStage, d = tmem + (2 * i + kst) * kKeys;
-  #pragma unroll
+                const uint32_t sb = (own + j) & 1;
+                const uint32_t q = sm + i * P::kQ, k = sm + P::kOffK + kst * P::kStage, d = tmem + (2 * i + sb) * kKeys;
+#pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                  tc_mma(d, desc_k(q + (x >> 2) * (128 * 128) + (x & 3) * 32), desc_k(k + (x >> 2) * (kKeys * 128) + (x & 3) * 32), kIdS,
-                         x > 0);
-                tc_commit(bar(kSFull + 2 * i + kst));
-                if (i == NRT - 1) tc_commit(bar(kKEmpty + kst));
+                  tc_mma(d, desc_k(q + (x >> 2) * (128 * 128) + (x & 3) * 32), desc_k(k + (x >> 2) * (kKeys * 128) + (x & 3) * 32),
+                         kIdS, x > 0);
+                tc_commit(bar(kSFull + 2 * i + sb));
+                if (i == tiles - 1) tc_commit(bar(kKEmpty + kst));
               }
               if (j > 0) {
-                const uint32_t f = g - 1, vst = f % P::kVStages, pst = f & 1;
-                mbar_wait(bar(kPFull + 2 * i + pst), (f >> 1) & 1, ok);
+                const uint32_t f = g - 1, vst = f % P::kVStages, of = own + j - 1, pb = of & 1;
+                mbar_wait(bar(kPFull + 2 * i + pb), (of >> 1) & 1, ok);
                 if (i == 0) mbar_wait(bar(kVFull + vst), (f / P::kVStages) & 1, ok);
                 tc_after();
-                const uint32_t v = sm + P::kOffV + vst * P::kStage, s = tmem + (2 * i + pst) * kKeys, o = tmem + P::kTmemO + i * D;
-  #pragma unroll
+                const uint32_t v = sm + P::kOffV + vst * P::kStage, s = tmem + (2 * i + pb) * kKeys, o = tmem + P::kTmemO + i * D;
+#pragma unroll
                 for (int x = 0; x < kKeys / 16; ++x)
                   tc_mma_ts(o, s + x * 8, desc_mn(v + x * 2048, kKeys * 128), kIdO, j > 1 || x > 0);
                 tc_commit(bar(kODone + i));
-                if (i == NRT - 1) tc_commit(bar(kVEmpty + vst));
+                if (i == tiles - 1) tc_commit(bar(kVEmpty + vst));
               }
             }
           }
           step += n;
+          own0 += n;
+          if (tiles > 1) own1 += n;
         }
       }
     }
@@ -449,7 +488,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     uint32_t phase = 0, step = 0;
     for (int piece = 0; walk.next(a, t, p); ++piece) {
       if (v && dt == 0) s_bad[(piece + 4) & 7] = INT32_MAX;  // (no warp is more than three pieces from another)
-      const int lim = min(p.sq.len, a.max_pages * a.page_size);
+      const int lim = p.lim;
       for (int j = p.t0; j < p.t1; ++j, ++step) {
         const uint32_t st = step % stages;
         mbar_wait(v ? bar(kVEmpty + st) : bar(kKEmpty + st), ((step / stages) & 1) ^ 1, ok);
@@ -476,12 +515,20 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     const uint32_t t_o = tmem + P::kTmemO + i * D + lanes;
     uint32_t step = 0;
     for (int piece = 0; walk.next(a, t, p); ++piece) {
+      if (i * 128 >= p.rows) continue;  // no rows in this tile
       const int fr = p.rt * P::kRows + i * 128 + row, tok = fr / t.group, gh = fr - tok * t.group;
-      const bool live = fr < p.sq.n * t.group;
-      const int see = live ? p.sq.len - p.sq.n + tok : -1;  // the last position that the row sees
+      bool live = fr < p.sq.n * t.group;
+      int see = live ? p.sq.len - p.sq.n + tok : -1;  // the last position that the row sees
+      if (t.shared && live) {
+        const int b = kv_seq_of(a, tok);
+        const Seq own = seq_at(a, max(b, 0));
+        live = b >= 0 && tok - own.row0 < own.n;
+        see = live ? min(own.len - own.n + tok - own.row0, p.lim - 1) : -1;
+      }
       const int64_t q_row = p.sq.row0 + tok, q_head = p.head * t.group + gh;
-      float c;
-      {  // queries, scaled by a power of two
+      float c = 0.f;
+      const bool warp_live = i * 128 + (warp & 3) * 32 < p.rows;
+      if (warp_live) {  // queries, scaled by a power of two
         const uint4* src = reinterpret_cast<const uint4*>(t.q + q_row * t.q_ts + q_head * t.q_hs);
         float big = 0.f;
         if (live) {
@@ -511,11 +558,18 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kQFull + i));
       }
-      // no key is hidden from any row of the warp before this step
-      const int first_row = p.rt * P::kRows + i * 128 + (warp & 3) * 32;
-      const int see_all = p.sq.len - p.sq.n + first_row / t.group;
+      if (lane == 0) mbar_arrive(bar(kQFull + i));
+      if (!warp_live) {  // nothing to do but to take part
+        for (int j = p.t0; j < p.t1; ++j, ++step) {
+          mbar_wait(bar(kSFull + 2 * i + (step & 1)), (step >> 1) & 1, ok);
+          if (step > 0) mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
+          if (lane == 0) mbar_arrive(bar(kPFull + 2 * i + (step & 1)));
+        }
+        mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
+        continue;
+      }
+      const int see_all = __reduce_min_sync(0xffffffffu, live ? see : INT32_MAX);  // up to here no key is hidden from a row of the warp
       float m = -INFINITY, l = 0.f;
       for (int j = p.t0; j < p.t1; ++j, ++step) {
         const uint32_t pst = step & 1, t_s = tmem + (2 * i + pst) * kKeys + lanes;
@@ -555,19 +609,22 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
           }
         }
         const float z = kPShift - (m == -INFINITY ? 0.f : m);
-        uint32_t ph[32];
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < kKeys; x += 2) {
-          const float e0 = ex2(fmaf(__uint_as_float(s[x >> 5][x & 31]), c, z));
-          const float e1 = ex2(fmaf(__uint_as_float(s[x >> 5][(x & 31) + 1]), c, z));
-          l4[(x >> 1) & 3] += e0 + e1;
-          ph[x >> 1] = pack2<false>(e0, e1);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t ph[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const float e0 = ex2(fmaf(__uint_as_float(s[h][x]), c, z));
+            const float e1 = ex2(fmaf(__uint_as_float(s[h][x + 1]), c, z));
+            l4[(x >> 1) & 3] += e0 + e1;
+            ph[x >> 1] = pack2<false>(e0, e1);
+          }
+          tc_st16(t_s + h * 16, ph);
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         // the previous step's product is done by now; seeing each one keeps the barrier's phase known
         if (step > 0) mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
-        tc_st32(t_s, ph);
         tc_wait_st();
         tc_before();
         __syncwarp();
@@ -581,9 +638,11 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
         if (lane == 0) kv_flag(a, MOE_KV_TIMEOUT);
         l = __uint_as_float(kNaN);
       }
-      const bool whole = p.t0 == 0 && p.t1 == p.steps;
+      const bool whole = p.t0 == 0 && p.t1 == p.steps, finish = whole && !t.shared;
+      const int64_t segment = (int64_t)p.head * W::row_tiles(t, p.sq) + p.rt;  // (with a shared prefix)
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const size_t at = ((size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * P::kRows + i * 128 + row;
+      const size_t at = (whole ? (size_t)segment : (size_t)blockIdx.x * 2 + (p.t0 > 0 ? 0 : 1)) * P::kRows + i * 128 + row;
+      float* partial = whole ? t.whole : t.partial;
       uint16_t* dst = t.out + q_row * t.o_ts + q_head * t.o_hs;
 #pragma unroll 1
       for (int x = 0; x < D; x += 32) {
@@ -596,11 +655,11 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
             float f[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[BITS == 8 ? k : (k & 1) * 4 + (k >> 1)] = __uint_as_float(o[y + k]);
-            if (whole) {
+            if (finish) {
               *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(pack2<BF16>(f[0] * inv, f[1] * inv), pack2<BF16>(f[2] * inv, f[3] * inv),
                                                                   pack2<BF16>(f[4] * inv, f[5] * inv), pack2<BF16>(f[6] * inv, f[7] * inv));
             } else {
-              float4* d4 = reinterpret_cast<float4*>(t.partial + at * D + x + y);
+              float4* d4 = reinterpret_cast<float4*>(partial + at * D + x + y);
               d4[0] = make_float4(f[0], f[1], f[2], f[3]);
               d4[1] = make_float4(f[4], f[5], f[6], f[7]);
             }
@@ -609,12 +668,17 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
         __syncwarp();
       }
       if (live) {
-        if (!whole)
-          t.stats[at] = make_float2(m, l);
+        if (!finish)
+          (whole ? t.whole_stats : t.stats)[at] = make_float2(m, l);
         else if (t.lse)
           t.lse[q_row * t.nq + q_head] = lse_of(m, l);
       }
-      if (tid == 0 && p.t0 > 0 && p.t1 == p.steps) t.ends[blockIdx.x] = SegmentEnd{p.first_part, p.b, p.head, p.rt};
+      if (tid == 0 && p.t1 == p.steps) {
+        if (t.shared)
+          t.spans[segment] = Span{whole ? kWhole : p.first_part, (int)blockIdx.x};
+        else if (!whole)
+          t.ends[blockIdx.x] = SegmentEnd{p.first_part, p.b, p.head, p.rt};
+      }
       tc_before();  // O and S have been read before the next piece's products, which wait for its queries or P
     }
   }

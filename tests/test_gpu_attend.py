@@ -28,16 +28,16 @@ def fill(cache, table, lens, kv_mul=1.0, dt=None, seed=0):
     return [(hk[at[i]:at[i + 1]], hv[at[i]:at[i + 1]]) for i in range(len(lens))]
 
 
-def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False):
+def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False, keys_rounded=False):
     """Per element.  A probability and a value are rounded to fp16 once each (2^-11 of the term; probabilities below
     fp16's normal range, which are held times 2^8, by 2^-33 of the largest), a score is off by delta <= (D / 16 + 4) 2^-21 of the
     sum of its products' magnitudes (fp32 accumulation of D / 16 steps, two scalings, the exponential), which moves a term by
-    2 delta relative; then half a step of the output's type.  With more than 64 rows a sequence the keys, integer times scale, are
-    rounded to fp16 too: delta grows by 2^-11 of the same sum."""
+    2 delta relative; then half a step of the output's type.  With more than 64 rows a sequence (16 of heads of 256), or behind a
+    shared prefix, the keys, integer times scale, are rounded to fp16 too: delta grows by 2^-11 of the same sum."""
     import torch
     D, at = q.shape[2], 0
     group = q.shape[1] // kv[0][0].shape[1]
-    keys_rounded = 2.0 ** -11 if max(news) * group > 64 else 0.0
+    keys_rounded = 2.0 ** -11 if keys_rounded or max(news) * group > (16 if D == 256 else 64) else 0.0
     eps = torch.finfo(dt).eps
     for (k, v), n, length in zip(kv, news, lens):
         if n == 0:
@@ -123,14 +123,14 @@ def test_many_sequences(seqs):
     run_case(8, 64, 32, 1, 2, [1] * seqs, [int(x) for x in rng.integers(1, 90, seqs)])
 
 
-@pytest.mark.parametrize("bits,dim", [(8, 128), (4, 256), (8, 64)])
+@pytest.mark.parametrize("bits,dim", [(8, 128), (4, 256), (8, 64), (4, 128), (8, 256), (4, 64)])
 def test_shared_prefix(bits, dim):
     """The hint changes nothing but the order of sums; a sequence may end inside the shared part."""
     import torch
     from quantized_expert_ffn_gemv_gb300 import attention
     page, share, hkv, group = 64, 256, 2, 4
     rng = np.random.default_rng(dim)
-    lens, news = [256 + 300, 257, 500, 100, 256, 0], [1, 1, 3, 1, 1, 0]
+    lens, news = [257, 500, 100, 256, 0, 256 + 300, 1, 40] + [260 + 13 * i for i in range(14)], [1, 3, 1, 1, 0, 1, 1, 2] + [1] * 14
     batch, table, n = make_batch(news, lens, page, rng, share=share // page, wide=1)
     cache = attention.KvCache(n, page, hkv, dim, bits)
     cache.data.fill_(0xFF)
@@ -151,7 +151,7 @@ def test_shared_prefix(bits, dim):
         lse = torch.zeros(batch.n_tokens, hkv * group).cuda()
         out = cache.attend(q, batch, lse=lse, shared_tokens=shared)
         cache.check()
-        check(f64(q), f64(out), f64(lse), kv, news, lens, dim ** -0.5, torch.bfloat16)
+        check(f64(q), f64(out), f64(lse), kv, news, lens, dim ** -0.5, torch.bfloat16, keys_rounded=shared > 0)
 
 
 def test_shared_prefix_of_a_large_batch():
@@ -175,7 +175,7 @@ def test_shared_prefix_of_a_large_batch():
     lse = torch.zeros(seqs, hkv * group).cuda()
     out = cache.attend(q, batch, lse=lse, shared_tokens=share)
     cache.check()
-    check(f64(q), f64(out), f64(lse), kv, [1] * seqs, lens, dim ** -0.5, torch.bfloat16)
+    check(f64(q), f64(out), f64(lse), kv, [1] * seqs, lens, dim ** -0.5, torch.bfloat16, keys_rounded=True)
 
 
 @pytest.mark.parametrize("n,group", [(1, 4), (3, 2), (100, 2)])
