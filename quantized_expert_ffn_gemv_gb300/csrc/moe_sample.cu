@@ -5,7 +5,8 @@
 // for a single row it is the chain of cluster barriers.
 //
 // Weights w = 2^-y, y = (max - z) log2(e) / T, are evaluated to about 2^-31
-// relative (float pairs for y, a 512-entry table and a cubic for the rest)
+// relative (float pairs for y, a 512-entry table and a cubic for the rest;
+// 2^-24 for a 16-bit logit nearer zero than 2^-13 of the maximum)
 // and summed as integers in units of 2^-45: integer sums have no order, so
 // any split of the work gives the same bits, and the sums that top-p, min-p
 // and the draw compare are exact.  Conversions go through the float's
@@ -82,29 +83,35 @@ __device__ __forceinline__ Rate rate_of(float T) {
   return r;
 }
 
-// y of a logit z <= m rounded to fp32, which orders logits weakly; infinity for -infinity.
-__device__ __forceinline__ float y_of(float z, float m, const Rate& c) { return z == -INFINITY ? INFINITY : (m - z) * c.h; }
-__device__ __forceinline__ int bin_of(float y) { return y < 64.f ? (int)(y * kPerOctave) : kBins - 1; }
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the low mantissa bits of a sum with it are the other term, rounded
+constexpr int kMagicBits = 0x4B400000;
 
-// w = W 2^-(31 + s - 1), W in 2^30 .. 2^31, s in 0 .. 64; W = 0 beyond 64 octaves.
+// y of a logit z <= m rounded to fp32, which orders logits weakly, at most
+// 100 (infinity for -infinity before the minimum); and its bin.
+__device__ __forceinline__ float y_of(float z, float m, const Rate& c) { return fminf((m - z) * c.h, 100.f); }
+__device__ __forceinline__ int bin_of(float y) { return min(__float_as_int(fmaf(y, (float)kPerOctave, kMagic)) - kMagicBits, kBins - 1); }
+
+// w = W 2^-(31 + s - 1), W in 2^30 .. 2^31.  From 64 octaves on W is
+// anything and s at least 64, which to_units makes 0.  EXACT: m - z is taken
+// with its rounding error; 16-bit logits need it only below 2^-13 of m.
+template <bool EXACT>
 __device__ __forceinline__ uint32_t weight31(float z, float m, const Rate& c, const float2* tab, int& s) {
-  const float yh = y_of(z, m, c);
-  if (!(yh < 64.f)) {
-    s = 64;
-    return 0;
+  const float x = m - z;
+  const float kf = fmaf(fminf(x * c.h, 100.f), (float)kTable, kMagic);  // (y_of's product)
+  const int k = __float_as_int(kf) - kMagicBits - 1;                    // round(512 y) - 1
+  // r = y - round(512 y) / 512, small, from y = (x + xl) (c.h + c.l)
+  float r = fmaf(x, c.h, (kf - kMagic) * (-1.f / kTable));
+  r = fmaf(x, c.l, r);
+  if (EXACT) {
+    const float bb = x - m;
+    r = fmaf((m - (x - bb)) + (-z - bb), c.h, r);  // m - z = x + that
   }
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low mantissa bits are the rounded integer
-  const float x = m - z, bb = x - m;
-  const float xl = (m - (x - bb)) + (-z - bb);  // m - z = x + xl
-  const float yl = fmaf(x, c.h, -yh) + fmaf(x, c.l, xl * c.h);
-  const float kf = fmaf(yh, (float)kTable, kMagic);
-  const int k = __float_as_int(kf) - 0x4B400001;  // round(512 y) - 1
-  const float r = (fmaf(kf - kMagic, -1.f / kTable, yh) + yl) * 0.693147180559945f;
-  const float p = r * fmaf(r, fmaf(r, -1.f / 6.f, 0.5f), -1.f);  // e^-r - 1
-  const float2 t = tab[k & (kTable - 1)];                        // t.x in 1/2 .. 1
+  // 2^-r - 1 by its series: |r| < 2^-10
+  const float p = r * fmaf(r, fmaf(r, -0.0555041087f, 0.2402265070f), -0.6931471806f);
+  const float2 t = tab[k & (kTable - 1)];  // t.x in 1/2 .. 1
   const float low = fmaf(fmaf(t.x, p, t.y), 2147483648.f, kMagic);
   s = (k >> 9) + 1;
-  return (((__float_as_uint(t.x) & 0x7FFFFFu) | 0x800000u) << 7) + (uint32_t)(__float_as_int(low) - 0x4B400000);
+  return (((__float_as_uint(t.x) & 0x7FFFFFu) | 0x800000u) << 7) + (uint32_t)(__float_as_int(low) - kMagicBits);
 }
 // W 2^(15 - s) rounded to units of 2^-45, with 32-bit shifts and one wide multiply.
 __device__ __forceinline__ uint64_t to_units(uint32_t W, int s) {
@@ -116,9 +123,10 @@ __device__ __forceinline__ uint64_t to_units(uint32_t W, int s) {
   asm("shr.u32 %0, %1, %2;" : "=r"(w) : "r"(W + (half >> 1)), "r"(down));
   return (uint64_t)w * mul;
 }
+template <bool EXACT>
 __device__ __forceinline__ uint64_t weight(float z, float m, const Rate& c, const float2* tab) {
   int s;
-  const uint32_t W = weight31(z, m, c, tab, s);
+  const uint32_t W = weight31<EXACT>(z, m, c, tab, s);
   return to_units(W, s);
 }
 
@@ -163,6 +171,7 @@ struct Entry {
   uint64_t w;
   uint32_t key, idx;
 };
+constexpr int kQueue = 64;  // logits a warp has waiting for their weights
 
 struct alignas(16) Shared {
   // this CTA's histogram, and later its lists: elements of the cut's bin, and in front of it
@@ -170,7 +179,8 @@ struct alignas(16) Shared {
     struct {
       uint32_t count[kBins], hi[kBins], lo[kBins];
     } h;
-    Entry part[2][kHalfList];
+    uint2 part[2][kHalfList];  // key, index
+    float queue[kSWarps][kQueue];
   };
   // first CTA: the cluster's histogram, and later the cluster's list
   union {
@@ -335,6 +345,7 @@ __device__ __forceinline__ void each(const Slice& v, F f) {
 // reaches top-p of it all.  The whole cluster calls it.  True: the token is
 // drawn.  Otherwise the cut is in the first CTA's Shared::cut until the
 // caller's next cluster barrier.
+template <bool EXACT>
 __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, const Slice& v, const Cut limit, bool limited,
                          bool by_mass) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -345,34 +356,32 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
   uint64_t before = 0, target = 0;  // mass in front of the range; the mass to reach (set at level 0)
   // is an element among those looked at, and in which bin
   auto place = [&](uint32_t idx, float z) -> int {
+    const int b0 = bin_of(y_of(z, v.m, v.c));
+    if (level == 0 && !limited) return b0;
     const uint32_t key = key_of(z);
     if (limited && !kept(key, idx, limit)) return -1;
-    const int b0 = bin_of(y_of(z, v.m, v.c));
     if (level == 0) return b0;
     return b0 == bin0 && key <= top_key && key >= low_key ? (int)((top_key - key) >> shift) : -1;
   };
   for (;;) {
     for (int i = tid; i < kBins; i += kSThreads) s.h.count[i] = s.h.hi[i] = s.h.lo[i] = 0;
     __syncthreads();
-    uint32_t far = 0;  // the last bin collects most elements when the temperature is low: counted apart (their mass is 0)
+    // counts, or masses.  The last bin collects most elements when the temperature is low: counted apart; its mass is taken for 0
+    uint32_t far = 0;
     each(v, [&](float z, uint32_t idx) {
       const int bin = place(idx, z);
       if (bin < 0) return;
-      if (bin == kBins - 1) {
+      if (by_mass) {
+        if (bin == kBins - 1) return;
+        int sh;
+        uint32_t W = weight31<EXACT>(z, v.m, v.c, s.pow2, sh);
+        W >>= sh - (level == 0 ? bin / kPerOctave : octave);  // relative to the bin's octave, which a weight is at most one below
+        atomicAdd(&s.h.hi[bin], W >> 16);
+        atomicAdd(&s.h.lo[bin], W & 0xFFFFu);
+      } else if (bin == kBins - 1) {
         ++far;
-        if (!by_mass) return;
       } else {
         atomicAdd(&s.h.count[bin], 1u);
-      }
-      if (by_mass) {
-        int sh;
-        uint32_t W = weight31(z, v.m, v.c, s.pow2, sh);
-        // relative to the bin's octave, which a weight is at most one below
-        W >>= min(sh - (level == 0 ? bin / kPerOctave : octave), 31);
-        if (W) {
-          atomicAdd(&s.h.hi[bin], W >> 16);
-          atomicAdd(&s.h.lo[bin], W & 0xFFFFu);
-        }
       }
     });
     far = __reduce_add_sync(0xffffffffu, far);
@@ -422,7 +431,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
           s.cut_need = need - cb;
           s.cut_before = mb;
         }
-        if (cnt[j] && (!by_mass || mass[j])) last = tid * kPer + j, last_before = mb, last_count = cnt[j];
+        if (by_mass ? mass[j] > 0 : cnt[j] > 0) last = tid * kPer + j, last_before = mb, last_count = cnt[j];
         cb += cnt[j];
         mb += mass[j];
       }
@@ -458,15 +467,15 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
     }
     if (count <= kList) {
       // list the bin's elements, and at level 0 those in front of it while they fit
-      const float y_end = bin0 == kBins - 1 ? INFINITY : (float)(bin0 + 1) / kPerOctave;
+      const float y_end = bin0 == kBins - 1 ? 100.f : (float)(bin0 + 1) / kPerOctave;
       each(v, [&](float z, uint32_t idx) {
-        if (!((v.m - z) * v.c.h <= y_end)) return;  // (most elements lie behind the bin)
+        if (y_of(z, v.m, v.c) > y_end) return;  // (most elements lie behind the bin)
         const int b = place(idx, z);
         if (b < 0 || (level == 0 && b > bin0)) return;
         const int sort = level == 0 && b < bin0;
         if (sort && s.part_n[1] > kHalfList) return;  // (a race that at most counts a few more)
         const uint32_t at = atomicAdd(&s.part_n[sort], 1u);
-        if (at < kHalfList) s.part[sort][at] = Entry{weight(z, v.m, v.c, s.pow2), key_of(z), idx};
+        if (at < kHalfList) s.part[sort][at] = make_uint2(key_of(z), idx);
       });
       cluster.sync();
       uint32_t n0 = 0, n1 = 0;
@@ -477,7 +486,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       }
       const bool whole0 = __all_sync(0xffffffffu, n0 <= kHalfList), whole1 = __all_sync(0xffffffffu, n1 <= kHalfList);
       const bool fits = level == 0 && whole0 && whole1 && __reduce_add_sync(0xffffffffu, n0 + n1) <= kList;
-      if (whole0) {
+      if (whole0 && __reduce_add_sync(0xffffffffu, n0) <= kList) {
         if (rank == 0) {
           // gather the CTAs' lists: one warp a list
           uint32_t mine = fits ? n0 + n1 : n0, start = mine;
@@ -494,7 +503,10 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
           const uint32_t len = sort ? (fits ? len1 : 0) : len0;
           if (r < C) {
             const Shared* o = cluster.map_shared_rank(&s, r);
-            for (uint32_t e = lane; e < len; e += 32) s.list[at + e] = o->part[sort][e];
+            for (uint32_t e = lane; e < len; e += 32) {
+              const uint2 x = o->part[sort][e];
+              s.list[at + e] = Entry{weight<EXACT>(logit_of(x.x), v.m, v.c, s.pow2), x.x, x.y};
+            }
           }
           if (tid == 0) s.found = 0;
           __syncthreads();
@@ -525,12 +537,12 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       }
     }
     if (one_key) {
-      // all `count` elements have the key top_key and one weight: the cut is the want-th of them in index order
+      // all elements of the bin have the key top_key and one weight: the cut is the want-th of them in index order
       const uint32_t k = top_key;
       uint32_t want = need;
       if (by_mass) {
-        const uint64_t w = weight(logit_of(k), v.m, v.c, s.pow2), more = target > before ? target - before : 1;
-        want = w ? (uint32_t)min((more + w - 1) / w, (uint64_t)count) : count;
+        const uint64_t w = weight<EXACT>(logit_of(k), v.m, v.c, s.pow2), more = target > before ? target - before : 1;
+        want = w ? (uint32_t)min((more + w - 1) / w, (uint64_t)UINT32_MAX) : UINT32_MAX;
       }
       const float* z = reinterpret_cast<const float*>(v.z);
       const int n = 4 * v.n4, seg = (n + kSWarps - 1) / kSWarps, lo = min(warp * seg, n), hi = min(lo + seg, n);
@@ -546,8 +558,13 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         s.ccount = all;
       }
       cluster.sync();
-      uint32_t front = 0;
-      for (int r = 0; r < rank; ++r) front += cluster.map_shared_rank(&s, r)->ccount;
+      uint32_t front = 0, equals = 0;
+      for (int r = 0; r < C; ++r) {
+        const uint32_t x = cluster.map_shared_rank(&s, r)->ccount;
+        front += r < rank ? x : 0;
+        equals += x;
+      }
+      want = min(want, equals);
       for (int x = 0; x < warp; ++x) front += s.wcnt[x];
       if (front < want && want <= front + mine) {
         for (int i0 = lo; i0 < hi; i0 += 32) {
@@ -647,6 +664,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   const int k0 = a.top_k ? a.top_k[row] : 0;
   const float p0 = a.top_p ? a.top_p[row] : 1.f, q0 = a.min_p ? a.min_p[row] : 0.f;
   const float u0 = a.u[row];
+  constexpr bool EXACT = sizeof(T) == 4;
 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -700,7 +718,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   bool limited = false;
   for (int step = 0; step < 2; ++step) {
     if (step == 0 ? !top_k : !top_p) continue;
-    if (find_cut(cluster, s, s0, v, cut, limited, step == 1)) return;  // drawn
+    if (find_cut<EXACT>(cluster, s, s0, v, cut, limited, step == 1)) return;  // drawn
     cut = s0->cut;
     limited = true;
     cluster.sync();
@@ -708,21 +726,48 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   // each warp's contiguous share of the slice, four neighbours a lane: its kept mass goes to wsum, the CTA's to ctotal
   const int seg = (n4 + kSWarps - 1) / kSWarps, lo = min(warp * seg, n4), hi = min(lo + seg, n4);
   const float z_cut = limited ? logit_of(cut.key) : -INFINITY;
-  auto kept_weight = [&](float zi, uint32_t idx) -> uint64_t {
-    if (zi < z_cut || (limited && !kept(key_of(zi), idx, cut))) return 0;
-    const uint64_t w = weight(zi, m, v.c, s.pow2);
+  auto is_kept = [&](float zi, uint32_t idx) { return zi >= z_cut && (!limited || kept(key_of(zi), idx, cut)); };
+  auto weigh = [&](float zi) -> uint64_t {
+    const uint64_t w = weight<EXACT>(zi, m, v.c, s.pow2);
     return w >= least ? w : 0;
   };
   auto load4 = [&](int i) { return i < hi ? v.z[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); };
   {
     uint64_t sum = 0;
-    for (int i0 = lo + lane; i0 < hi; i0 += 64) {
-      const float4 q[2] = {load4(i0), load4(i0 + 32)};
+    if (!limited) {
+      for (int i0 = lo + lane; i0 < hi; i0 += 64) {
+        const float4 q[2] = {load4(i0), load4(i0 + 32)};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t idx = base + 4 * (i0 + 32 * j);
-        sum += kept_weight(q[j].x, idx) + kept_weight(q[j].y, idx + 1) + kept_weight(q[j].z, idx + 2) + kept_weight(q[j].w, idx + 3);
+        for (int j = 0; j < 2; ++j) sum += (weigh(q[j].x) + weigh(q[j].y)) + (weigh(q[j].z) + weigh(q[j].w));
       }
+    } else {
+      // few of many are kept: they queue up for their weights, a warp's lanes full at a time
+      __syncthreads();  // (the queues lie where the lists were)
+      float* queue = s.queue[warp];
+      int waiting = 0;
+      for (int i0 = lo; i0 < hi; i0 += 32) {
+        const float4 q = load4(i0 + lane);
+        const float zs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool k = is_kept(zs[e], base + 4 * (i0 + lane) + e);
+          const unsigned b = __ballot_sync(0xffffffffu, k);
+          if (!b) continue;
+          if (k) queue[waiting + __popc(b & ((1u << lane) - 1u))] = zs[e];
+          waiting += __popc(b);
+          if (waiting >= 32) {
+            __syncwarp();
+            const float z0 = queue[lane], z1 = queue[32 + lane];
+            sum += weigh(z0);
+            waiting -= 32;
+            __syncwarp();
+            if (lane < waiting) queue[lane] = z1;
+            __syncwarp();
+          }
+        }
+      }
+      __syncwarp();
+      if (lane < waiting) sum += weigh(queue[lane]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -752,7 +797,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
       const uint32_t idx = base + 4 * (i0 + lane);
       uint64_t w[4], incl = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) incl += w[e] = kept_weight(zs[e], idx + e);
+      for (int e = 0; e < 4; ++e) incl += w[e] = i0 + lane < hi && is_kept(zs[e], idx + e) ? weigh(zs[e]) : 0;
       const uint64_t four = incl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
