@@ -19,9 +19,13 @@
 // into.  Each CTA lists its elements of that bin and those in front of it.
 // If both fit one list, the first CTA ranks them all and draws the token by
 // itself; if only the bin's do, it ranks those for the cut's last element
-// and the cluster draws; otherwise the bin's range of logits is histogrammed
-// again, finer, until few are left or all have the same logit, whose cut is
-// then an index.
+// and the cluster draws; otherwise the bin is histogrammed again, a thousand
+// times finer in y and then by the logits' bits, until few are left or all
+// have the same logit, whose cut is then an index.  The histogram's bound is
+// its shared-memory atomics (10 us for the counts of 256 rows' elements, an SM
+// having two), so for a small k a histogram of each thread's largest logit is
+// tried first: the k-th largest of those is at most the k-th of all, and
+// seldom many lie between.
 #include <cooperative_groups.h>
 #include <cmath>
 
@@ -35,7 +39,8 @@ namespace {
 constexpr int kSThreads = 512, kSWarps = kSThreads / 32;
 constexpr int kBins = 1024, kPerOctave = 16;  // 64 octaves: beyond them a weight is 0 in units of 2^-45
 constexpr int kUnit = 45;                     // 2^18 weights of 2^45 fit 64 bits
-constexpr int kList = 512;                    // elements ranked against each other at most: one a thread
+constexpr int kList = kSThreads;              // elements sorted at most: one a thread
+constexpr int kDirect = 256;                  // up to here each element is compared with all others, beyond they are sorted
 constexpr int kHalfList = 384;                // what a CTA lists of either sort
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxCluster = 8;
@@ -167,10 +172,11 @@ struct Cut {
 };
 __device__ __forceinline__ bool kept(uint32_t key, uint32_t idx, const Cut& c) { return key > c.key || (key == c.key && idx <= c.idx); }
 
-struct Entry {
-  uint64_t w;
-  uint32_t key, idx;
-};
+// An element of a list by its place in the order: larger first.
+__device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t idx) { return (uint64_t)key << 32 | ~idx; }
+__device__ __forceinline__ uint32_t key_in(uint64_t e) { return (uint32_t)(e >> 32); }
+__device__ __forceinline__ uint32_t idx_in(uint64_t e) { return ~(uint32_t)e; }
+
 constexpr int kQueue = 64;  // logits a warp has waiting for their weights
 
 struct alignas(16) Shared {
@@ -179,19 +185,21 @@ struct alignas(16) Shared {
     struct {
       uint32_t count[kBins], hi[kBins], lo[kBins];
     } h;
-    uint2 part[2][kHalfList];  // key, index
+    uint64_t part[2][kHalfList];
     float queue[kSWarps][kQueue];
   };
-  // first CTA: the cluster's histogram, and later the cluster's list
+  // first CTA: the cluster's histogram, and later the cluster's list and what sorting it takes
   union {
     struct {
       uint64_t mass[kBins];
       uint32_t count[kBins];
     } all;
-    Entry list[kList];
+    struct {
+      uint64_t list[kList], w[kList], swap[2][kList];
+    };
   };
   float2 pow2[kTable];
-  uint64_t wsum[kSWarps];
+  uint64_t wsum[kSWarps], bsum[kSWarps];
   uint32_t wcnt[kSWarps];
   float wmax[kSWarps];
   // written by the CTA, read by the cluster
@@ -201,10 +209,9 @@ struct alignas(16) Shared {
   uint64_t ctotal;
   // written by the first CTA, read by the cluster
   int cut_bin;
-  uint32_t cut_count, cut_need;
+  uint32_t cut_count, cut_need, cut_front;
   uint64_t cut_before, cut_target;
   Cut cut;
-  int found;
 };
 
 // Exclusive prefixes of a count and a mass over the block's threads.
@@ -255,66 +262,125 @@ struct Slice {
   float p;        // top-p, 1 = all
   uint64_t least; // min-p in units
   float u;
+  float top;  // the largest of this thread's own
   int32_t* token;
   float* prob;
 };
 
-// Ranks the list's n <= kList elements against each other: place = how many
-// are ahead of this thread's element in the order, front = their mass.  With
-// few elements several neighbouring threads share one: thread t has element t / share of
-// n, and all of the sharers get its result.
-__device__ __forceinline__ void rank_list(const Shared& s, int n, int& share, uint32_t& place, uint64_t& front) {
-  share = 1;
-  while (share < 32 && n * share * 2 <= kSThreads) share *= 2;
-  const int e = threadIdx.x / share, part = threadIdx.x % share;
-  place = 0;
-  front = 0;
-  if (e < n) {
-    const Entry me = s.list[e];
-    const uint64_t rank = (uint64_t)me.key << 32 | ~me.idx;
-#pragma unroll 4
-    for (int i = part; i < n; i += share) {
-      const Entry o = s.list[i];
-      if (((uint64_t)o.key << 32 | ~o.idx) > rank) ++place, front += o.w;
+// Sorts one value a thread, descending, over the block's first P threads (P a
+// power of two from 32; the others have 0): a bitonic network, by shuffles
+// within a warp and through shared memory across.
+__device__ __forceinline__ uint64_t sort_values(Shared& s, uint64_t v, int P) {
+  const int tid = threadIdx.x;
+  int buf = 0;
+  for (int size = 2; size <= P; size *= 2) {
+    const bool down = (tid & size) == 0;
+    for (int stride = size / 2; stride >= 32; stride /= 2) {
+      s.swap[buf][tid] = v;
+      __syncthreads();
+      const uint64_t o = s.swap[buf][tid ^ stride];
+      v = (((tid & stride) == 0) == down) == (o > v) ? o : v;
+      buf ^= 1;  // (the next barrier is behind every read of this one)
+    }
+    if (tid < P) {
+#pragma unroll
+      for (int stride = 16; stride > 0; stride /= 2) {
+        if (stride >= size) continue;
+        const uint64_t o = __shfl_xor_sync(0xffffffffu, v, stride);
+        v = (((tid & stride) == 0) == down) == (o > v) ? o : v;
+      }
     }
   }
+  return v;
+}
+
+// A thread's element of a list in the first CTA: its weight, how many are
+// ahead of it in the order, and their mass.  Threads without one have w = 0
+// and a place behind all.
+struct Ranked {
+  uint64_t e, w, front;
+  uint32_t place;
+};
+// How many neighbouring threads share an element of a list compared directly.
+__device__ __forceinline__ int sharers(int n) {
+  int share = 1;
+  while (share < 32 && n * share * 2 <= kSThreads) share *= 2;
+  return share;
+}
+// The sum of w over the list's elements before(i, mine), this thread's part by part.
+template <typename F>
+__device__ __forceinline__ uint64_t sum_before(const Shared& s, int n, int share, F before, uint32_t& ahead) {
+  uint64_t sum = 0;
+  ahead = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x % share; i < n; i += share)
+    if (before(s.list[i])) ++ahead, sum += s.w[i];
   for (int o = 1; o < share; o <<= 1) {
-    place += __shfl_xor_sync(0xffffffffu, place, o);
-    front += __shfl_xor_sync(0xffffffffu, front, o);
+    ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
+  return sum;
+}
+// Ranks the list's n <= kList elements.  500 of them take 18 us by comparing
+// all with all and 3 by sorting; 50 take 2 and 4.
+template <bool EXACT>
+__device__ __forceinline__ Ranked rank_list(Shared& s, const Slice& v, int n) {
+  const int tid = threadIdx.x;
+  Ranked r{tid < n ? s.list[tid] : 0, 0, 0, (uint32_t)tid};
+  if (n > kDirect) r.e = sort_values(s, r.e, 1 << (32 - __clz(n - 1)));
+  if (tid < n) r.w = weight<EXACT>(logit_of(key_in(r.e)), v.m, v.c, s.pow2);
+  if (n > kDirect) {
+    uint32_t none = 0;
+    r.front = r.w;
+    block_scan(s, none, r.front);
+    return r;
+  }
+  if (tid < n) s.w[tid] = r.w;
+  __syncthreads();
+  const int share = sharers(n), mine = tid / share;
+  r.e = mine < n ? s.list[mine] : 0;
+  r.front = sum_before(s, n, share, [&](uint64_t o) { return o > r.e; }, r.place);
+  r.w = mine < n && tid % share == 0 ? s.w[mine] : 0;
+  if (mine >= n || tid % share) r.place = kList;
+  return r;
 }
 
 // The first CTA alone: every element that top-k and top-p can keep is in the
 // list, n of them; cut them, and draw the token.  target: the mass that top-p
 // asks for, or 0: its share of what top-k keeps of the list.
+template <bool EXACT>
 __device__ void draw_from_list(Shared& s, const Slice& v, int n, uint64_t target) {
-  int share;
-  uint32_t place;
-  uint64_t front, w = 0;
-  rank_list(s, n, share, place, front);
-  const int e = threadIdx.x / share, part = threadIdx.x % share;
-  if (e < n && !(v.k > 0 && place >= v.k)) w = s.list[e].w;
+  const int tid = threadIdx.x;
+  const Ranked r = rank_list<EXACT>(s, v, n);
+  uint64_t w = v.k > 0 && r.place >= v.k ? 0 : r.w;
   if (v.p < 1.f) {
     // front < sum * p  <=>  front < ceil(sum * p)
-    if (!target) target = max(mul_frac(block_sum(s, part == 0 ? w : 0), v.p, true), (uint64_t)1);
-    if (front >= target) w = 0;
+    if (!target) target = max(mul_frac(block_sum(s, w), v.p, true), (uint64_t)1);
+    if (r.front >= target) w = 0;
   }
-  if (w < v.least && place != 0) w = 0;
-  const uint64_t total = block_sum(s, part == 0 ? w : 0);  // (its barriers: all have read the list)
-  if (e < n && part == 0) s.list[e].w = w;
-  __syncthreads();
+  if (w < v.least && r.place != 0) w = 0;
+  const uint64_t total = block_sum(s, w);  // (its barriers: all have read the list)
+  uint64_t below, e = r.e;
+  if (n > kDirect) {  // the kept ones in index order, each with its place in the list
+    s.w[tid] = w;
+    const uint64_t i = sort_values(s, w ? (uint64_t)(uint32_t)e << 32 | tid : 0, 1 << (32 - __clz(n - 1)));
+    __syncthreads();
+    w = i ? s.w[(uint32_t)i] : 0;
+    e = i >> 32;
+    below = w;
+    uint32_t none = 0;
+    block_scan(s, none, below);
+  } else {
+    const int share = sharers(n), mine = tid / share;
+    if (tid % share == 0 && mine < n) s.w[mine] = w;
+    __syncthreads();
+    uint32_t ahead;
+    below = sum_before(s, n, share, [&](uint64_t o) { return (uint32_t)o > (uint32_t)e; }, ahead);  // (~index)
+  }
   // running sum > u * total  <=>  running sum > floor(u * total)
   const uint64_t at = mul_frac(total, v.u, false);
-  uint32_t idx = 0;
-  uint64_t below = 0;
-  if (e < n) {
-    idx = s.list[e].idx;
-#pragma unroll 4
-    for (int i = part; i < n; i += share) below += s.list[i].idx < idx ? s.list[i].w : 0;
-  }
-  for (int o = 1; o < share; o <<= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
-  if (part == 0 && w != 0 && below <= at && at < below + w) {
-    *v.token = (int32_t)idx;
+  if (w != 0 && below <= at && at < below + w) {
+    *v.token = (int32_t)idx_in(e);
     if (v.prob) *v.prob = (float)w / (float)total;
   }
 }
@@ -340,6 +406,31 @@ __device__ __forceinline__ void each(const Slice& v, F f) {
   }
 }
 
+// The same for the logits that pred accepts, when they are few: a thread goes
+// through the ones among its eight, instead of all threads through all eight.
+template <typename P, typename F>
+__device__ __forceinline__ void each_of(const Slice& v, P pred, F f) {
+  for (int i0 = threadIdx.x; i0 < v.n4; i0 += 2 * kSThreads) {
+    float4 q[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      q[j] = i0 + j * kSThreads < v.n4 ? v.z[i0 + j * kSThreads] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    uint32_t hit = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      hit |= (pred(q[j].x) ? 1u : 0u) << 4 * j;
+      hit |= (pred(q[j].y) ? 2u : 0u) << 4 * j;
+      hit |= (pred(q[j].z) ? 4u : 0u) << 4 * j;
+      hit |= (pred(q[j].w) ? 8u : 0u) << 4 * j;
+    }
+    if (i0 + kSThreads >= v.n4) hit &= 15u;
+    for (; hit; hit &= hit - 1) {
+      const int b = __ffs(hit) - 1, at = 4 * (i0 + (b >> 2) * kSThreads) + (b & 3);
+      f(reinterpret_cast<const float*>(v.z)[at], v.base + at);
+    }
+  }
+}
+
 // The cut among the elements that `limit` keeps (all, when not limited): at
 // the top-k'th of the order, or, by mass, at the first where the running mass
 // reaches top-p of it all.  The whole cluster calls it.  True: the token is
@@ -350,25 +441,34 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
                          bool by_mass) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
-  int level = 0, shift = 0, octave = 0, bin0 = 0;
-  uint32_t top_key = 0, low_key = 0;  // level > 0: the range of keys looked at
+  int level = 0, shift = 0, octave = 0, bin0 = 0, bin1 = 0;  // level 0 looks at all, 1 at bin0 of it, 2 and up at bin1 of that
+  float y0 = 0.f, finer = 0.f;                               // level 1: where its bins begin, bins an octave
+  uint32_t top_key = 0, low_key = 0;                         // level 2 and up: the range of keys looked at
+  bool quick = !by_mass && !limited && v.k * 4 <= (uint32_t)(kSThreads * C);  // only the threads' largest
   uint32_t need = v.k;
   uint64_t before = 0, target = 0;  // mass in front of the range; the mass to reach (set at level 0)
   // is an element among those looked at, and in which bin
   auto place = [&](uint32_t idx, float z) -> int {
-    const int b0 = bin_of(y_of(z, v.m, v.c));
+    const float y = y_of(z, v.m, v.c);
+    const int b0 = bin_of(y);
+    if (level > 0 && b0 != bin0) return -1;
     if (level == 0 && !limited) return b0;
     const uint32_t key = key_of(z);
     if (limited && !kept(key, idx, limit)) return -1;
     if (level == 0) return b0;
-    return b0 == bin0 && key <= top_key && key >= low_key ? (int)((top_key - key) >> shift) : -1;
+    const int b1 = min((int)((y - y0) * finer), kBins - 2);
+    if (level == 1) return b1;
+    return b1 == bin1 && key <= top_key && key >= low_key ? (int)((top_key - key) >> shift) : -1;
   };
   for (;;) {
     for (int i = tid; i < kBins; i += kSThreads) s.h.count[i] = s.h.hi[i] = s.h.lo[i] = 0;
     __syncthreads();
     // counts, or masses.  The last bin collects most elements when the temperature is low: counted apart; its mass is taken for 0
     uint32_t far = 0;
-    each(v, [&](float z, uint32_t idx) {
+    if (quick) {
+      const int bin = bin_of(y_of(v.top, v.m, v.c));
+      if (bin < kBins - 1) atomicAdd(&s.h.count[bin], 1u);
+    } else each(v, [&](float z, uint32_t idx) {
       const int bin = place(idx, z);
       if (bin < 0) return;
       if (by_mass) {
@@ -391,12 +491,15 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
     for (int i = rank * (kBins / C) + tid; i < (rank + 1) * (kBins / C); i += kSThreads) {
       uint32_t cnt = 0;
       uint64_t mass = 0;
-      for (int r = 0; r < C; ++r) {
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= C) continue;
         const Shared* o = cluster.map_shared_rank(&s, r);
         cnt += o->h.count[i];
-        mass += ((uint64_t)o->h.hi[i] << 16) + o->h.lo[i];
+        if (by_mass) mass += ((uint64_t)o->h.hi[i] << 16) + o->h.lo[i];
       }
-      s0->all.count[i] = cnt;
+      // (a relative weight is at most 2^30 1.022: by mass a lower bound of the count)
+      s0->all.count[i] = by_mass ? (uint32_t)((mass >> 30) - (mass >> 35)) : cnt;
       s0->all.mass[i] = (mass << (kUnit - 30)) >> (level == 0 ? i / kPerOctave : octave);
     }
     if (tid < 2) s.part_n[tid] = 0;
@@ -429,6 +532,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
           s.cut_bin = tid * kPer + j;
           s.cut_count = cnt[j];
           s.cut_need = need - cb;
+          s.cut_front = cb;
           s.cut_before = mb;
         }
         if (by_mass ? mass[j] > 0 : cnt[j] > 0) last = tid * kPer + j, last_before = mb, last_count = cnt[j];
@@ -436,7 +540,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         mb += mass[j];
       }
       __syncthreads();
-      if (s.cut_bin < 0) {  // the bins' masses, each rounded down, end a little below the target: the last bin that counts
+      if (s.cut_bin < 0 && !quick) {  // the bins' masses, each rounded down, end a little below the target: the last bin that counts
         const int best = __reduce_max_sync(0xffffffffu, last);
         if (lane == 0) s.wcnt[warp] = (uint32_t)(best + 1);
         __syncthreads();
@@ -446,36 +550,51 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
           s.cut_bin = last;
           s.cut_count = last_count;
           s.cut_need = last_count;
+          s.cut_front = kList + 1;
           s.cut_before = last_before;
         }
       }
     }
     cluster.sync();
     const int bin = s0->cut_bin;
-    const uint32_t count = s0->cut_count;
+    const uint32_t count = quick ? 0 : s0->cut_count;
+    if (quick && bin < 0) {  // (too few of them have a weight)
+      quick = false;
+      cluster.sync();  // the cut's bin has been read
+      continue;
+    }
+    const bool front_too = quick || level == 0 && s0->cut_front + count <= kList;  // (by mass, maybe not)
     before = s0->cut_before;
     if (by_mass) target = s0->cut_target;
-    if (!by_mass) need = s0->cut_need;
-    const bool one_key = level > 0 && shift == 0;
+    if (!by_mass && !quick) need = s0->cut_need;
+    const bool one_key = level > 1 && shift == 0;
     if (level == 0) {
       bin0 = bin;
       octave = bin / kPerOctave;
+      y0 = ((float)bin0 - 0.5f) / kPerOctave;
+      finer = bin0 == kBins - 1 ? 27.f : 16000.f;  // 1,000 for the bin; the last one ends at 100
+    } else if (level == 1) {
+      bin1 = bin;
     } else {
       top_key -= (uint32_t)bin << shift;
       const uint32_t span = shift ? (1u << shift) - 1u : 0u;
       low_key = top_key - low_key > span ? top_key - span : low_key;
     }
     if (count <= kList) {
-      // list the bin's elements, and at level 0 those in front of it while they fit
+      // list the bin's elements, and at level 0 those in front of it where they may fit
       const float y_end = bin0 == kBins - 1 ? 100.f : (float)(bin0 + 1) / kPerOctave;
-      each(v, [&](float z, uint32_t idx) {
-        if (y_of(z, v.m, v.c) > y_end) return;  // (most elements lie behind the bin)
+      const float y_begin = front_too ? 0.f : ((float)bin0 - 0.5f) / kPerOctave;
+      const auto near = [&](float z) {
+        const float y = y_of(z, v.m, v.c);
+        return y >= y_begin && y <= y_end;
+      };
+      each_of(v, near, [&](float z, uint32_t idx) {
         const int b = place(idx, z);
-        if (b < 0 || (level == 0 && b > bin0)) return;
+        if (b < 0 || (level == 0 && b > bin0) || (level == 1 && b != bin1)) return;
         const int sort = level == 0 && b < bin0;
-        if (sort && s.part_n[1] > kHalfList) return;  // (a race that at most counts a few more)
+        if (*(volatile uint32_t*)&s.part_n[sort] > kHalfList) return;  // (a race that at most counts a few more)
         const uint32_t at = atomicAdd(&s.part_n[sort], 1u);
-        if (at < kHalfList) s.part[sort][at] = make_uint2(key_of(z), idx);
+        if (at < kHalfList) s.part[sort][at] = entry(key_of(z), idx);
       });
       cluster.sync();
       uint32_t n0 = 0, n1 = 0;
@@ -485,8 +604,8 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         n1 = o->part_n[1];
       }
       const bool whole0 = __all_sync(0xffffffffu, n0 <= kHalfList), whole1 = __all_sync(0xffffffffu, n1 <= kHalfList);
-      const bool fits = level == 0 && whole0 && whole1 && __reduce_add_sync(0xffffffffu, n0 + n1) <= kList;
-      if (whole0 && __reduce_add_sync(0xffffffffu, n0) <= kList) {
+      const bool fits = front_too && whole0 && whole1 && __reduce_add_sync(0xffffffffu, n0 + n1) <= kList;
+      if (quick ? fits : whole0 && __reduce_add_sync(0xffffffffu, n0) <= kList) {
         if (rank == 0) {
           // gather the CTAs' lists: one warp a list
           uint32_t mine = fits ? n0 + n1 : n0, start = mine;
@@ -503,38 +622,30 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
           const uint32_t len = sort ? (fits ? len1 : 0) : len0;
           if (r < C) {
             const Shared* o = cluster.map_shared_rank(&s, r);
-            for (uint32_t e = lane; e < len; e += 32) {
-              const uint2 x = o->part[sort][e];
-              s.list[at + e] = Entry{weight<EXACT>(logit_of(x.x), v.m, v.c, s.pow2), x.x, x.y};
-            }
+            for (uint32_t e = lane; e < len; e += 32) s.list[at + e] = o->part[sort][e];
           }
-          if (tid == 0) s.found = 0;
           __syncthreads();
           if (fits) {
-            draw_from_list(s, v, to, by_mass ? target : 0);
+            draw_from_list<EXACT>(s, v, to, by_mass ? target : 0);
           } else {
-            int share;
-            uint32_t ahead;
-            uint64_t front;
-            rank_list(s, to, share, ahead, front);
-            front += before;
-            const int e = tid / share;
-            if (e < to) {
-              const Entry me = s.list[e];
-              // the need-th; or the one whose weight takes the mass to the target (the last, should rounding leave none)
-              if (by_mass ? front < target && (target <= front + me.w || ahead == (uint32_t)to - 1) : ahead == need - 1) {
-                s.cut = Cut{me.key, me.idx};
-                s.found = 1;
-              }
-            }
-            __syncthreads();
-            // what lies in front of the bin may have reached the target by rounding: then its first element is the cut
-            if (!s.found && e < to && ahead == 0) s.cut = Cut{s.list[e].key, s.list[e].idx};
+            const Ranked r = rank_list<EXACT>(s, v, to);
+            // the need-th; or the one whose weight takes the mass to the target: the
+            // first or the last where rounding has put the target before or behind them
+            const uint64_t front = before + r.front;
+            const bool first = r.place == 0, last = r.place == (uint32_t)to - 1;
+            if (r.place < (uint32_t)to && (by_mass ? (first || front < target) && (last || target <= front + r.w) : r.place == need - 1))
+              s.cut = Cut{key_in(r.e), idx_in(r.e)};
           }
         }
         cluster.sync();
         return fits;
       }
+    }
+    if (quick) {
+      quick = false;
+      before = 0;
+      cluster.sync();  // the lists' lengths have been read
+      continue;
     }
     if (one_key) {
       // all elements of the bin have the key top_key and one weight: the cut is the want-th of them in index order
@@ -577,11 +688,11 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       cluster.sync();
       return false;
     }
-    // the bin again, finer: first the keys it spans
-    if (level == 0) {
+    // the bin again, finer: from level 2 on within the keys it spans
+    if (level == 1) {
       uint32_t hi = 0, lo = 0xFFFFFFFFu;
       each(v, [&](float z, uint32_t idx) {
-        if (place(idx, z) == bin0) hi = max(hi, key_of(z)), lo = min(lo, key_of(z));
+        if (place(idx, z) == bin1) hi = max(hi, key_of(z)), lo = min(lo, key_of(z));
       });
       hi = __reduce_max_sync(0xffffffffu, hi);
       lo = __reduce_min_sync(0xffffffffu, lo);
@@ -601,7 +712,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       low_key = lo;
     }
     shift = 0;
-    while (((top_key - low_key) >> shift) >= (uint32_t)(kBins - 1)) ++shift;  // the far bin stays free
+    while (level > 0 && ((top_key - low_key) >> shift) >= (uint32_t)(kBins - 1)) ++shift;  // the far bin stays free
     ++level;
     cluster.sync();  // ccount, cfirst, the lists' lengths and the cut have been read
   }
@@ -628,11 +739,12 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   // the one read: scalar up to a 16-byte boundary, 16 bytes a thread from there
   constexpr int kVec = 16 / sizeof(T);
   float top = -INFINITY;
-  auto put = [&](int i, float v) {
+  auto clean = [&](float v) {
     v = v != v ? -INFINITY : v;  // a NaN ranks below every number and weighs nothing, like -infinity
-    z[i] = v;
     top = fmaxf(top, v);
+    return v;
   };
+  auto put = [&](int i, float v) { z[i] = clean(v); };
   const int head = min(n, (int)(((16 - ((uintptr_t)src & 15)) & 15) / sizeof(T)));
   const int vecs = (n - head) / kVec;
   if (tid < head) put(tid, as_f32(src[tid]));
@@ -650,8 +762,15 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
       const int v = v0 + j * kSThreads + tid;
       if (v < vecs) {
         const T* e = reinterpret_cast<const T*>(&w[j]);
+        if (head == 0) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) put(head + v * kVec + i, as_f32(e[i]));
+          for (int i = 0; i < kVec; i += 4)
+            reinterpret_cast<float4*>(z + v * kVec)[i / 4] =
+                make_float4(clean(as_f32(e[i])), clean(as_f32(e[i + 1])), clean(as_f32(e[i + 2])), clean(as_f32(e[i + 3])));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) put(head + v * kVec + i, as_f32(e[i]));
+        }
       }
     }
   }
@@ -666,9 +785,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   const float u0 = a.u[row];
   constexpr bool EXACT = sizeof(T) == 4;
 
+  float wtop = top;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s.wmax[warp] = top;
+  for (int o = 16; o > 0; o >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
+  if (lane == 0) s.wmax[warp] = wtop;
   __syncthreads();
   if (tid == 0) {
     float v = s.wmax[0];
@@ -705,6 +825,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     return;
   }
   if (m == INFINITY) {  // infinite logits share the weight
+    top = top == INFINITY ? 0.f : -INFINITY;
     for (int i = tid; i < n; i += kSThreads) z[i] = z[i] == INFINITY ? 0.f : -INFINITY;
     m = 0.f;
     __syncthreads();
@@ -712,7 +833,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   const bool top_k = k0 > 1 && k0 < a.vocab, top_p = p0 < 1.f;
   const uint64_t least = q0 > 0.f ? (q0 >= 1.f ? 1ull << kUnit : mul_frac(1ull << kUnit, q0, true)) : 0;
   const Slice v{reinterpret_cast<const float4*>(z), n4, base, m, rate_of(fminf(fmaxf(T0, 1e-30f), 1e30f)), top_k ? (uint32_t)k0 : 0,
-                top_p ? p0 : 1.f, least, u0 > 0.f ? fminf(u0, 0.99999994f) : 0.f, a.tokens + row, a.probs ? a.probs + row : nullptr};
+                top_p ? p0 : 1.f, least, u0 > 0.f ? fminf(u0, 0.99999994f) : 0.f, top, a.tokens + row, a.probs ? a.probs + row : nullptr};
 
   Cut cut{0, 0xFFFFFFFFu};
   bool limited = false;
@@ -787,24 +908,35 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     total += __shfl_xor_sync(0xffffffffu, total, o);
     front += __shfl_xor_sync(0xffffffffu, front, o);
   }
-  for (int w = 0; w < warp; ++w) front += s.wsum[w];
   // sum > u * total  <=>  sum > floor(u * total)
   const uint64_t at = mul_frac(total, v.u, false);
-  if (front <= at && at < front + s.wsum[warp]) {
-    for (int i0 = lo; i0 < hi && front <= at; i0 += 32) {
-      const float4 q = load4(i0 + lane);
+  int of = 0;  // the warp whose share holds the token, if this CTA's does
+  while (of < kSWarps && !(front <= at && at < front + s.wsum[of])) front += s.wsum[of++];
+  if (of < kSWarps) {
+    // all warps take that share, 32 float4 each at a time
+    const int first = min(of * seg, n4), end = min(first + seg, n4);
+    for (int i0 = first; i0 < end; i0 += 32 * kSWarps) {
+      const int i = i0 + 32 * warp + lane;
+      const float4 q = i < end ? v.z[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       const float zs[4] = {q.x, q.y, q.z, q.w};
-      const uint32_t idx = base + 4 * (i0 + lane);
+      const uint32_t idx = base + 4 * i;
       uint64_t w[4], incl = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) incl += w[e] = i0 + lane < hi && is_kept(zs[e], idx + e) ? weigh(zs[e]) : 0;
+      for (int e = 0; e < 4; ++e) incl += w[e] = i < end && is_kept(zs[e], idx + e) ? weigh(zs[e]) : 0;
       const uint64_t four = incl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
       }
+      __syncthreads();
+      if (lane == 31) s.bsum[warp] = incl;
+      __syncthreads();
       uint64_t below = front + incl - four;
+      for (int w2 = 0; w2 < kSWarps; ++w2) {
+        below += w2 < warp ? s.bsum[w2] : 0;
+        front += s.bsum[w2];
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (below <= at && at < below + w[e]) {
@@ -813,7 +945,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         }
         below += w[e];
       }
-      front += __shfl_sync(0xffffffffu, incl, 31);
+      if (front > at) break;
     }
   }
   cluster.sync();
