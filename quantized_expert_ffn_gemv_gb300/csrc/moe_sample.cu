@@ -177,8 +177,6 @@ __device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t idx) { return (
 __device__ __forceinline__ uint32_t key_in(uint64_t e) { return (uint32_t)(e >> 32); }
 __device__ __forceinline__ uint32_t idx_in(uint64_t e) { return ~(uint32_t)e; }
 
-constexpr int kQueue = 64;  // logits a warp has waiting for their weights
-
 struct alignas(16) Shared {
   // this CTA's histogram, and later its lists: elements of the cut's bin, and in front of it
   union {
@@ -186,7 +184,6 @@ struct alignas(16) Shared {
       uint32_t count[kBins], hi[kBins], lo[kBins];
     } h;
     uint64_t part[2][kHalfList];
-    float queue[kSWarps][kQueue];
   };
   // first CTA: the cluster's histogram, and later the cluster's list and what sorting it takes
   union {
@@ -408,13 +405,14 @@ __device__ __forceinline__ void each(const Slice& v, F f) {
 
 // The same for the logits that pred accepts, when they are few: a thread goes
 // through the ones among its eight, instead of all threads through all eight.
-template <typename P, typename F>
-__device__ __forceinline__ void each_of(const Slice& v, P pred, F f) {
-  for (int i0 = threadIdx.x; i0 < v.n4; i0 += 2 * kSThreads) {
+// STEP threads go through the float4 from first, this thread's, to end.
+template <int STEP, typename P, typename F>
+__device__ __forceinline__ void each_of(const Slice& v, int first, int end, P pred, F f) {
+  for (int i0 = first; i0 < end; i0 += 2 * STEP) {
     float4 q[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      q[j] = i0 + j * kSThreads < v.n4 ? v.z[i0 + j * kSThreads] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      q[j] = i0 + j * STEP < end ? v.z[i0 + j * STEP] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     uint32_t hit = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -423,9 +421,9 @@ __device__ __forceinline__ void each_of(const Slice& v, P pred, F f) {
       hit |= (pred(q[j].z) ? 4u : 0u) << 4 * j;
       hit |= (pred(q[j].w) ? 8u : 0u) << 4 * j;
     }
-    if (i0 + kSThreads >= v.n4) hit &= 15u;
+    if (i0 + STEP >= end) hit &= 15u;
     for (; hit; hit &= hit - 1) {
-      const int b = __ffs(hit) - 1, at = 4 * (i0 + (b >> 2) * kSThreads) + (b & 3);
+      const int b = __ffs(hit) - 1, at = 4 * (i0 + (b >> 2) * STEP) + (b & 3);
       f(reinterpret_cast<const float*>(v.z)[at], v.base + at);
     }
   }
@@ -588,7 +586,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         const float y = y_of(z, v.m, v.c);
         return y >= y_begin && y <= y_end;
       };
-      each_of(v, near, [&](float z, uint32_t idx) {
+      each_of<kSThreads>(v, tid, v.n4, near, [&](float z, uint32_t idx) {
         const int b = place(idx, z);
         if (b < 0 || (level == 0 && b > bin0) || (level == 1 && b != bin1)) return;
         const int sort = level == 0 && b < bin0;
@@ -862,33 +860,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         for (int j = 0; j < 2; ++j) sum += (weigh(q[j].x) + weigh(q[j].y)) + (weigh(q[j].z) + weigh(q[j].w));
       }
     } else {
-      // few of many are kept: they queue up for their weights, a warp's lanes full at a time
-      __syncthreads();  // (the queues lie where the lists were)
-      float* queue = s.queue[warp];
-      int waiting = 0;
-      for (int i0 = lo; i0 < hi; i0 += 32) {
-        const float4 q = load4(i0 + lane);
-        const float zs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool k = is_kept(zs[e], base + 4 * (i0 + lane) + e);
-          const unsigned b = __ballot_sync(0xffffffffu, k);
-          if (!b) continue;
-          if (k) queue[waiting + __popc(b & ((1u << lane) - 1u))] = zs[e];
-          waiting += __popc(b);
-          if (waiting >= 32) {
-            __syncwarp();
-            const float z0 = queue[lane], z1 = queue[32 + lane];
-            sum += weigh(z0);
-            waiting -= 32;
-            __syncwarp();
-            if (lane < waiting) queue[lane] = z1;
-            __syncwarp();
-          }
-        }
-      }
-      __syncwarp();
-      if (lane < waiting) sum += weigh(queue[lane]);
+      each_of<32>(v, lo + lane, hi, [&](float zi) { return zi >= z_cut; },
+                  [&](float zi, uint32_t idx) { sum += is_kept(zi, idx) ? weigh(zi) : 0; });
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
