@@ -177,14 +177,16 @@ MOE_API moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch
  *   out = softmax(scale * q k^T over positions <= the token's) v
  * Query head j reads kv head j / (n_q / n_kv_heads).  Scores, softmax
  * statistics and sums are fp32; probabilities and dequantised values enter
- * the products as fp16.  lse (fp32 [n_tokens][n_q], or NULL): the natural
+ * the products as fp16, as do, with many rows or behind a shared prefix,
+ * keys without their block's scale.  lse (fp32 [n_tokens][n_q], or NULL): the natural
  * logarithm of the sum of exp(score).  A token of negative position sees
  * nothing: its out is 0 and its lse -infinity.  A row that meets a bad page
  * is NaN.  What lies in pages behind the position a row sees never reaches that row.
  * shared_tokens (a multiple of page_size, 0 = off) says that the block tables
  * of all sequences begin with the same pages up to that position, so that
- * those keys may be read once for the whole batch.  Results equal those of
- * shared_tokens = 0 up to rounding.
+ * those keys may be read once for the whole batch, which is done where it
+ * spares reads of 160 MB or more.  Results equal those of shared_tokens = 0 up
+ * to rounding.
  * workspace: device, 16-byte aligned, of moe_kv_attend_workspace bytes; its
  * contents need no preparation and mean nothing afterwards.  Calls that
  * overlap need workspaces of their own.
@@ -211,7 +213,7 @@ MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_bat
  *          exceeds u times the kept sum
  * temperature <= 0 is greedy: the first of the order.  A NaN parameter is
  * taken as off (temperature: greedy).  Weights are evaluated to about 2^-31
- * relative and summed as integers (units of 2^-45 of the largest), so results
+ * relative (2^-24 for a 16-bit logit nearer zero than 2^-13 of the maximum) and summed as integers (units of 2^-45 of the largest), so results
  * do not depend on the order of execution.  Temperatures are clamped to
  * 1e-30..1e30.  A maximum of +infinity: equal weight for every infinite
  * logit, none for the rest.  A row without a number above -infinity has no

@@ -2,6 +2,8 @@
 // the merge of partial results and the C entries.  The kernels:
 //   attend_rows_kernel  (moe_attend_rows.cuh)   few rows a sequence, mma.sync
 //   attend_tiles_kernel (moe_attend_tiles.cuh)  many rows a sequence, tcgen05
+#include <algorithm>
+
 #include "moe_attend.cuh"
 
 namespace moe {
@@ -14,7 +16,6 @@ using namespace ptx;
 // (WARPS 8) a CTA takes one row, its warps every eighth part; many segments
 // have a part or two each: then (WARPS 1) every warp takes a row.
 constexpr int kJoinThreads = 256;
-constexpr int kSharedTiles = 2;  // row tiles from which a shared prefix gets a pass of its own
 
 template <int D, bool BF16, int WARPS>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const KvArgs a, const AttArgs t) {
@@ -265,9 +266,17 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   p->tile_rows = p->tiles ? big : rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32;
   p->parts = p->tiles ? sms : sms * rows_blocks(dim, cache->bits, p->tile_rows);
   p->max_row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
-  // A prefix is worth a pass of its own when the batch's rows would read it several times over.
+  // A prefix gets a pass of its own where that spares 160 MB of reads, which
+  // take as long as the pass and the merge of its results.  In us, with the
+  // pass and without: 32 sequences x 4,096 tokens (heads of 128, 8 bits, 4 kv
+  // heads: 138 MB) 42 and 37, 64 x 2,048 42 and 40, 16 x 16,384 (267 MB) 42
+  // and 56, 48 x 16,384 (802 MB) 60 and 109; 4 bits 64 x 4,096 (147 MB) 43 and
+  // 51; heads of 256, 4 bits, 2 kv heads, 16 x 16,384 (142 MB) 61 and 44, 16 x
+  // 32,768 65 and 70; heads of 64, 8 kv heads, 64 x 4,096 (281 MB) 40 and 62.
   const int64_t all_rows = (int64_t)batch->n_tokens * group;
-  p->shared = !p->tiles && all_rows > kSharedTiles * p->tile_rows ? shared_tokens : 0;
+  const int64_t passes = std::max<int64_t>(all_rows / p->tile_rows, std::min(batch->n_seqs, batch->n_tokens));
+  const double spared = (double)(passes - 1) * shared_tokens * heads * (dim * cache->bits / 4 + dim / 8);
+  p->shared = !p->tiles && spared >= 160e6 ? shared_tokens : 0;
   p->pre_parts = sms;
   p->pre_rows = big;
   const int64_t segments = (int64_t)batch->n_seqs * heads * p->max_row_tiles, pre_segments = heads * ((all_rows + big - 1) / big);

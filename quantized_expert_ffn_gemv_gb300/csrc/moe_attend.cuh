@@ -113,12 +113,6 @@ __device__ __forceinline__ float score_factor(float scale_log2, int e) {
   return scale_log2 == 0.f ? 1.f : fmaxf(fabsf(scale_log2) * pow2i(e), FLT_MIN);
 }
 
-// Host: shared memory of a kernel, raised to what it needs.
-template <typename K>
-bool raise_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
 // Launches, one translation unit each (moe_attend_rows8.cu and so on).  The
 // number of CTAs an SM holds is part of the plan.
 int rows_blocks(int dim, int bits, int tile_rows);

@@ -571,7 +571,8 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
 template <int D, int BITS, bool BF16, int NT>
 moe_status_t launch_rows_kernel(const KvArgs& kv, const AttArgs& t, cudaStream_t st) {
   constexpr int smem = RowsPlan<D, BITS, NT>::kSmem;
-  if (!raise_smem(attend_rows_kernel<D, BITS, BF16, NT>, smem)) return MOE_ERR_CUDA;
+  const moe_status_t ok = raise_smem<attend_rows_kernel<D, BITS, BF16, NT>>(smem);
+  if (ok != MOE_OK) return ok;
   attend_rows_kernel<D, BITS, BF16, NT><<<t.parts, kAttThreads, smem, st>>>(kv, t);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

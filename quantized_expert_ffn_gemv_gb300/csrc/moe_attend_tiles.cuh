@@ -692,8 +692,9 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
 template <int D, int BITS, bool BF16>
 moe_status_t launch_tiles_kernel(const KvArgs& kv, const AttArgs& t, cudaStream_t st) {
   using P = TilesPlan<D, BITS>;
-  const auto kernel = attend_tiles_kernel<D, BITS, BF16>;
-  if (!raise_smem(kernel, P::kSmem)) return MOE_ERR_CUDA;
+  constexpr auto kernel = attend_tiles_kernel<D, BITS, BF16>;
+  const moe_status_t ok = raise_smem<kernel>(P::kSmem);
+  if (ok != MOE_OK) return ok;
   // the roles' registers come out of the launch's: with fewer the softmax would wait for its share for good
   static int enough = 0;
   if (!__atomic_load_n(&enough, __ATOMIC_RELAXED)) {

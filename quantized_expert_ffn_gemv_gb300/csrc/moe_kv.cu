@@ -43,7 +43,6 @@ bool out_heads_ok(const moe_heads_t* h, int n_heads, int n_tokens, int dim) {
 }
 
 moe_status_t device_sms(int* sms) {
-  constexpr int kMaxDevices = 64;
   static int known[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;

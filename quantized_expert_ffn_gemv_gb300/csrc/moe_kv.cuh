@@ -79,7 +79,20 @@ __device__ __forceinline__ uint8_t* kv_tile_of(const KvArgs& a, int b, int pos, 
 moe_status_t kv_args(const moe_kv_cache_t* c, const moe_kv_batch_t* b, KvArgs* out);
 bool heads_ok(const moe_heads_t* h, int dim);
 bool out_heads_ok(const moe_heads_t* h, int n_heads, int n_tokens, int dim);
+constexpr int kMaxDevices = 64;
 moe_status_t device_sms(int* sms);
+// Raises the shared memory that a kernel may use on the current device, once a
+// device; always to the same size, so that calls at the same time agree.
+template <auto KERNEL>
+moe_status_t raise_smem(int bytes) {
+  static int raised[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
+  if (__atomic_load_n(&raised[dev], __ATOMIC_RELAXED) >= bytes) return MOE_OK;
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return MOE_ERR_CUDA;
+  __atomic_store_n(&raised[dev], bytes, __ATOMIC_RELAXED);
+  return MOE_OK;
+}
 
 template <bool BF16>
 __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {

@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
 template <typename T>
 moe_status_t launch_sample(SampleArgs a, cudaStream_t st) {
   int sms = 0;
-  const moe_status_t ok = device_sms(&sms);
+  moe_status_t ok = device_sms(&sms);
   if (ok != MOE_OK) return ok;
   // Slices of at most 80 KB leave room for two CTAs an SM; few rows take larger
   // clusters, down to slices of 4,096, so that one row's read and passes are
@@ -937,8 +937,8 @@ moe_status_t launch_sample(SampleArgs a, cudaStream_t st) {
   while (C < kMaxCluster && (int64_t)a.rows * C * 2 <= sms && a.vocab / C > 4096) C *= 2;
   a.slice = (((a.vocab + C - 1) / C) + 7) & ~7;  // a multiple of the float4 and of 16 bytes of any type
   const int smem = (int)sizeof(Shared) + a.slice * 4;
-  if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  ok = raise_smem<sample_kernel<T>>((int)sizeof(Shared) + kMaxVocab / kMaxCluster * 4);
+  if (ok != MOE_OK) return ok;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.rows * C));
   cfg.blockDim = dim3(kSThreads);

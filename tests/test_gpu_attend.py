@@ -178,6 +178,75 @@ def test_shared_prefix_of_a_large_batch():
     check(f64(q), f64(out), f64(lse), kv, [1] * seqs, lens, dim ** -0.5, torch.bfloat16, keys_rounded=True)
 
 
+def shared_case(bits, dim, hkv, group, share, seqs, seed=0):
+    """Sequences of 1 to share + 70 positions, most longer than share, one to three new tokens each, some none; their first
+    pages are the same.  Returns (cache, batch, table, q, kv, news, lens)."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import attention
+    rng = np.random.default_rng(seed)
+    page = 64
+    lens = [share + int(x) for x in rng.integers(1, 70, seqs)]
+    news = [1] * seqs
+    lens[3:8], news[3:8] = [share, 1, share - 5, 0, share + 2], [1, 1, 3, 0, 3]
+    news[11], news[20] = 0, 2
+    batch, table, n = make_batch(news, lens, page, rng, share=share // page, wide=1)
+    cache = attention.KvCache(n, page, hkv, dim, bits)
+    cache.data.fill_(0xFF)
+    base = torch.randn(2, share, hkv, dim, device="cuda").bfloat16()
+    cache.append(base[0], base[1], whole(table[:1], [share]))
+    tails = [max(0, x - share) for x in lens]
+    own = torch.randn(2, sum(tails), hkv, dim, device="cuda").bfloat16()
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    cu = np.concatenate(([0], np.cumsum(tails)))
+    cache.append(own[0], own[1], attention.KvBatch(dev(table.tolist()), dev(lens), dev(cu.tolist()), int(cu[-1]), max(tails)))
+    cache.check()
+    hb, ho = [ref.held(f64(x), bits) for x in base], [ref.held(f64(x), bits) for x in own]
+    kv = [tuple(np.concatenate((hb[j][:min(share, x)], ho[j][cu[i]:cu[i + 1]])) for j in (0, 1)) for i, x in enumerate(lens)]
+    q = (torch.randn(batch.n_tokens, hkv * group, dim, device="cuda") * 2).bfloat16()
+    return cache, batch, table, q, kv, news, lens
+
+
+@pytest.mark.parametrize("bits,dim,group,share,seqs", [(8, 128, 2, 1024, 170), (4, 256, 2, 1024, 170), (8, 64, 3, 1920, 180),
+                                                       (4, 128, 5, 1984, 160), (8, 256, 1, 576, 160), (4, 64, 2, 1920, 330)])
+def test_shared_prefix_read_once(bits, dim, group, share, seqs):
+    """Enough reads spared for a pass of its own: seqs * share * 4 heads of more than 160 MB."""
+    import torch
+    assert (seqs * 0.9) * share * 4 * (dim * bits / 4 + dim / 8) > 160e6
+    cache, batch, _, q, kv, news, lens = shared_case(bits, dim, 4, group, share, seqs)
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    out = cache.attend(q, batch, lse=lse, shared_tokens=share)
+    cache.check()
+    check(f64(q), f64(out), f64(lse), kv, news, lens, dim ** -0.5, torch.bfloat16, keys_rounded=True)
+
+
+def test_shared_prefix_captured_and_with_a_bad_page():
+    """Replays and a call on another stream agree with the eager call bit for bit; a page out of range makes NaN of what sees it."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import moe
+    share = 1024
+    cache, batch, table, q, _, news, lens = shared_case(8, 128, 4, 2, share, 170)
+    eager = cache.attend(q, batch, shared_tokens=share)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = cache.attend(q, batch, shared_tokens=share, stream=s)
+    s.synchronize()
+    out, g = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        cache.attend(q, batch, out=out, shared_tokens=share)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(eager, other) and torch.equal(eager, out) and eager.isfinite().all()
+    batch._tensors[0][:, 2] = 2 ** 30  # positions 128 to 191 of all
+    bad = cache.attend(q, batch, shared_tokens=share)
+    with pytest.raises(moe.MoeError, match="bad page"):
+        cache.check()
+    at = 0
+    for n, length in zip(news, lens):
+        if n:
+            assert bad[at:at + n].isnan().all() if length > 192 else torch.equal(bad[at:at + n], eager[at:at + n])
+        at += n
+
 @pytest.mark.parametrize("n,group", [(1, 4), (3, 2), (100, 2)])
 def test_rows_that_see_nothing(n, group):
     """More new tokens than positions: the first rows see nothing, out 0 and lse -infinity; the batch is flagged."""
