@@ -72,7 +72,7 @@ MOE_API moe_status_t moe_rope_table(int32_t n_positions, int32_t rot_dim, double
  * negative position is padding: its rows of q_out and k_out stay as they
  * were.  A position of n_positions or more has no angle: its rows are NaN.
  * dtype: MOE_BF16 or MOE_FP16.
- * Errors: INVALID_ARG (NULL or misaligned pointers, bad sizes, strides or eps), UNSUPPORTED (dtype MOE_FP32), CUDA.
+ * Errors: INVALID_ARG (NULL or misaligned pointers, bad sizes, strides or eps), UNSUPPORTED (dtype MOE_FP32, over 65535 heads), CUDA.
  */
 MOE_API moe_status_t moe_qk_norm_rope(const moe_norm_rope_t* desc, int32_t dtype, int32_t n_tokens, int32_t head_dim,
                                       int32_t n_q, const moe_heads_t* q, const moe_heads_t* q_out, int32_t n_kv,
@@ -185,7 +185,7 @@ MOE_API moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch
  * shared_tokens (a multiple of page_size, 0 = off) says that the block tables
  * of all sequences begin with the same pages up to that position, so that
  * those keys may be read once for the whole batch, which is done where it
- * spares reads of 160 MB or more.  Results equal those of shared_tokens = 0 up
+ * spares reading a million keys.  Results equal those of shared_tokens = 0 up
  * to rounding.
  * workspace: device, 16-byte aligned, of moe_kv_attend_workspace bytes; its
  * contents need no preparation and mean nothing afterwards.  Calls that

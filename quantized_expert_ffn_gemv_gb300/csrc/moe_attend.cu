@@ -266,17 +266,17 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   p->tile_rows = p->tiles ? big : rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32;
   p->parts = p->tiles ? sms : sms * rows_blocks(dim, cache->bits, p->tile_rows);
   p->max_row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
-  // A prefix gets a pass of its own where that spares 160 MB of reads, which
-  // take as long as the pass and the merge of its results.  In us, with the
-  // pass and without: 32 sequences x 4,096 tokens (heads of 128, 8 bits, 4 kv
-  // heads: 138 MB) 42 and 37, 64 x 2,048 42 and 40, 16 x 16,384 (267 MB) 42
-  // and 56, 48 x 16,384 (802 MB) 60 and 109; 4 bits 64 x 4,096 (147 MB) 43 and
-  // 51; heads of 256, 4 bits, 2 kv heads, 16 x 16,384 (142 MB) 61 and 44, 16 x
-  // 32,768 65 and 70; heads of 64, 8 kv heads, 64 x 4,096 (281 MB) 40 and 62.
+  // A prefix gets a pass of its own where that spares the rows' kernel a
+  // million keys (counted a kv head); the pass and the merge of its results
+  // take as long.  In us, with the pass and without (where all but the first
+  // read come from L2), 8 bits, heads of 128, 4 kv heads: 64 sequences x 2,048
+  // tokens (0.5 million) 42 and 33, 16 x 16,384 (1.0) 42 and 43, 64 x 4,096
+  // (1.0) 45 and 48, 128 x 4,096 (2.1) 53 and 85, 48 x 16,384 (3.1) 57 and 108.
+  // 4 bits, 64 x 4,096: 43 and 48; heads of 256, 2 kv heads, 16 x 16,384 (0.5)
+  // 61 and 41, 16 x 32,768 (1.0) 66 and 68; of 64, 8 kv heads, 64 x 4,096 (2.1) 40 and 58.
   const int64_t all_rows = (int64_t)batch->n_tokens * group;
   const int64_t passes = std::max<int64_t>(all_rows / p->tile_rows, std::min(batch->n_seqs, batch->n_tokens));
-  const double spared = (double)(passes - 1) * shared_tokens * heads * (dim * cache->bits / 4 + dim / 8);
-  p->shared = !p->tiles && spared >= 160e6 ? shared_tokens : 0;
+  p->shared = !p->tiles && (double)(passes - 1) * shared_tokens * heads >= 0.98e6 ? shared_tokens : 0;
   p->pre_parts = sms;
   p->pre_rows = big;
   const int64_t segments = (int64_t)batch->n_seqs * heads * p->max_row_tiles, pre_segments = heads * ((all_rows + big - 1) / big);

@@ -76,184 +76,225 @@ struct RowArgs {
   const float* table;
   const int32_t* positions;
   int n_positions, rot, inter;
-  float eps, woff;
-  int n_tokens, nq, nk, dim, slots;  // slots: units of a token
+  float eps, woff, inv_dim;
+  int n_tokens, nq, nk, dim;
+  int per, q_slots, k_slots;  // heads a unit takes; units of a token for q, and for k (and for v)
 };
 
-// x [8] of a scale block's 4 lanes -> the block's fp16 scale, and this lane's
-// 8 integers packed (8 bytes, or 4 bytes in x of the result).
-template <int BITS>
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint16_t& scale) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);  // a NaN is above infinity, infinity above every number
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+  float2 r;
+  unpack2<BF16>(w, r.x, r.y);
+  return r;
+}
+
+// One element's integer from its quotient by d, and its half-even tie from the exact rest.
+__device__ __forceinline__ uint32_t quantise_slowly(float x, float d, float inv, float low, float top) {
+  float q = rintf(x * inv);
+  const float rest = fmaf(-q, d, x);
+  if (fabsf(rest) * 2.f == d && q != 2.f * rintf(0.5f * q)) q += copysignf(1.f, rest);
+  q = d > 0.f ? fminf(fmaxf(q, low), top) : 0.f;
+  return (uint32_t)(int)q;
+}
+
+// w, 8 values packed, of a scale block's 4 lanes -> the block's fp16 scale, and
+// this lane's 8 integers packed (8 bytes, or 4 bytes in x of the result).
+template <bool BF16, int BITS>
+__device__ __forceinline__ uint2 quantise8(const uint32_t (&w)[4], uint16_t& scale) {
+  // the largest magnitude, as the type's bits: a NaN is above infinity, infinity above every number
+  uint32_t big = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 2));
+  const float m = pair_of<BF16>(max(big >> 16, big & 0xFFFFu)).x;
   constexpr float top = BITS == 8 ? 127.f : 7.f, low = BITS == 8 ? -127.f : -8.f;
-  constexpr int bias = BITS == 8 ? 128 : 8;
-  scale = __half_as_ushort(__float2half_rn(__uint_as_float(m) / top));
-  if (m > 0x477E0000u) scale = 0x7FFFu;  // above 65024 (NaN and infinity among them): the block reads back as NaN
+  scale = __half_as_ushort(__float2half_rn(m / top));
+  if (!(m <= 65024.f)) scale = 0x7FFFu;  // the block reads back as NaN
   const float d = __half2float(__ushort_as_half(scale));
   // round_half_even(x / d) without eight divisions.  x and d have at most 11
   // significant bits and the quotient's half-integers h / 2 at most 8, so
   // 2 x = h d or the two are 2^-19 apart, relative: x * (1 / d), off by less
   // than 2^-22, rounds as the quotient does unless that is a half-integer
-  // exactly.  Then |x - q d| = d / 2 (an exact fma), and an odd q goes to its even neighbour.
-  const float inv = d > 0.f ? 1.f / d : 0.f;
+  // exactly.  Then |x - q d| = d / 2 (an exact fma), and an odd q goes to its
+  // even neighbour.  A normal d is within 2^-11 of m / top, which keeps |q|
+  // within top; the sum with 1.5 * 2^23 rounds and holds q in its low bits.
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
+  constexpr float kMagic = 12582912.f;
   uint32_t u[8];
+  float far = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float q = rintf(x[j] * inv);
-    const float rest = fmaf(-q, d, x[j]);
-    if (fabsf(rest) * 2.f == d && q != 2.f * rintf(0.5f * q)) q += copysignf(1.f, rest);
-    q = d > 0.f ? fminf(fmaxf(q, low), top) : 0.f;
-    u[j] = (uint32_t)((int)q + bias);
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = pair_of<BF16>(w[j]);
+    const float2 y = fma2(x, make_float2(inv, inv), make_float2(kMagic, kMagic));
+    const float qx = kMagic - y.x, qy = kMagic - y.y;  // -q
+    far = fmaxf(far, fmaxf(fabsf(fmaf(qx, d, x.x)), fabsf(fmaf(qy, d, x.y))));
+    u[2 * j] = __float_as_uint(y.x);
+    u[2 * j + 1] = __float_as_uint(y.y);
   }
-  if (BITS == 8)
-    return make_uint2(u[0] | u[1] << 8 | u[2] << 16 | u[3] << 24, u[4] | u[5] << 8 | u[6] << 16 | u[7] << 24);
-  uint32_t w = 0;
+  if (!(d >= 6.103515625e-05f) || far * 2.f == d) {
+    const float slow = d > 0.f ? 1.f / d : 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w |= u[j] << (4 * j);
-  return make_uint2(w, 0u);
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = pair_of<BF16>(w[j]);
+      u[2 * j] = quantise_slowly(x.x, d, slow, low, top);
+      u[2 * j + 1] = quantise_slowly(x.y, d, slow, low, top);
+    }
+  }
+  // the low bytes of four words, in order
+  const auto bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t e) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, e, 0x0040), 0x5410);
+  };
+  if (BITS == 8) return make_uint2(bytes(u[0], u[1], u[2], u[3]) ^ 0x80808080u, bytes(u[4], u[5], u[6], u[7]) ^ 0x80808080u);
+  const uint32_t even = bytes(u[0], u[2], u[4], u[6]), odd = bytes(u[1], u[3], u[5], u[7]);
+  return make_uint2(((even & 0x0F0F0F0Fu) | (odd << 4 & 0xF0F0F0F0u)) ^ 0x88888888u, 0u);
 }
 
 // LPR lanes a row.  NORM: q and k rows are normalised and rotated.  BITS > 0:
 // k and v rows go to the cache (else k goes to ko and there is no v).
+// blockIdx.y is a unit's place within its token, so that all of a block's
+// rows are q, k or v rows and what they share (weights, angles) is prepared
+// once a unit: with 4 rows a unit the kernel is bound by the instructions it
+// issues.  4,096 tokens with 76 MB of q and k in heads of 256 take 18 us (24 with
+// rows of all three kinds side by side, each preparing its own).
 template <int LPR, bool BF16, bool NORM, int BITS>
 __global__ void __launch_bounds__(kRowThreads, 4) head_rows_kernel(const RowArgs r, const KvArgs kv) {
   constexpr bool STORE = BITS > 0;
   const int lane = threadIdx.x % LPR;
-  const uint32_t unit = blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR;
-  const int t = (int)(unit / (uint32_t)r.slots), s = (int)(unit % (uint32_t)r.slots);
-  const int H = r.nq + r.nk + (STORE ? r.nk : 0);
+  const int t = blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR;
+  int slot = blockIdx.y;
+  const int kind = slot < r.q_slots ? 0 : slot < r.q_slots + r.k_slots ? 1 : 2;
+  const bool flags = STORE && slot == 0 && lane == 0;
+  slot -= kind == 0 ? 0 : kind == 1 ? r.q_slots : r.q_slots + r.k_slots;
+  const int h0 = slot * r.per, n = min(r.per, (kind == 0 ? r.nq : r.nk) - h0);  // the unit's heads
+  const HeadSrc src = kind == 0 ? r.q : kind == 1 ? r.k : r.v;
   bool live = t < r.n_tokens;
   const bool in = lane * 8 < r.dim;
+
+  uint4 x[kRowsPerUnit];
+  const uint16_t* from = src.p + (int64_t)t * src.ts + h0 * src.hs + lane * 8;
+#pragma unroll
+  for (int i = 0; i < kRowsPerUnit; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (live && in && i < n) x[i] = *reinterpret_cast<const uint4*>(from + i * src.hs);
+  }
+
   int pos = 0;
   uint8_t* tile = nullptr;
   if (STORE && live) {
     const int b = kv_seq_of(kv, t);
     live = b >= 0;
     if (live) {
-      const int c0 = __ldg(kv.cu + b), n = __ldg(kv.cu + b + 1) - c0, len = __ldg(kv.lens + b);
-      pos = len - n + (t - c0);
+      const int c0 = __ldg(kv.cu + b), fresh = __ldg(kv.cu + b + 1) - c0, len = __ldg(kv.lens + b);
+      pos = len - fresh + (t - c0);
       if (pos >= 0) tile = kv_tile_of(kv, b, pos, kv_tile_bytes(LPR * 8, BITS));
-      if (lane == 0 && s == 0) {
-        const int bad = (n > len || n > kv.max_tokens ? MOE_KV_BAD_BATCH : 0) | (pos >= 0 && !tile ? MOE_KV_BAD_PAGE : 0);
+      if (flags) {
+        const int bad = (fresh > len || fresh > kv.max_tokens ? MOE_KV_BAD_BATCH : 0) | (pos >= 0 && !tile ? MOE_KV_BAD_PAGE : 0);
         if (bad) kv_flag(kv, bad);
       }
     }
   }
   const int row = pos & (kKvTile - 1);
-  int angle = pos;
-  if (NORM && live && r.positions) angle = __ldg(r.positions + t);
-  if (NORM && angle < 0) live = false;  // padding
-
-  uint4 x[kRowsPerUnit];
-#pragma unroll
-  for (int i = 0; i < kRowsPerUnit; ++i) {
-    const int h = s + i * r.slots;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (live && in && h < H) {
-      const HeadSrc& src = h < r.nq ? r.q : h < r.nq + r.nk ? r.k : r.v;
-      const int hh = h < r.nq ? h : h < r.nq + r.nk ? h - r.nq : h - r.nq - r.nk;
-      x[i] = *reinterpret_cast<const uint4*>(src.p + (int64_t)t * src.ts + hh * src.hs + lane * 8);
-    }
-  }
-  // cos and sin of this lane's 8 elements (a pair shares one)
-  float cs[8], sn[8];
-  int partner = lane;
-  float sign = 0.f, nan_pos = 0.f;
+  const bool turns = NORM && kind < 2;
   const int half8 = r.rot / 16;  // lanes of the rotated part's first half
-  if (NORM && r.rot > 0 && live) {
-    if (angle >= r.n_positions) {
-      nan_pos = __uint_as_float(0x7FFFFFFFu);
-    } else if (lane < 2 * half8) {
+  const bool rotated = turns && lane < 2 * half8;
+  const int partner = rotated && !r.inter ? (lane < half8 ? lane + half8 : lane - half8) : lane;
+  // out = inv * (x * cw + g * sw): g is the rotation's partner of x, cw and sw hold the weights, cos and +-sin
+  float2 cw[4], sw[4];
+  float nan_pos = 0.f;
+  if (NORM) {
+    int angle = pos;
+    if (live && r.positions) angle = __ldg(r.positions + t);
+    if (angle < 0) live = false;  // padding
+    const uint16_t* wt = kind == 0 ? r.wq : r.wk;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cw[j] = sw[j] = make_float2(1.f, 1.f);
+    if (turns && wt != nullptr && in) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(wt + lane * 8)), b = __ldg(reinterpret_cast<const uint4*>(wt + partner * 8));
+      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cw[j] = pair_of<BF16>(wa[j]);
+        cw[j].x += r.woff, cw[j].y += r.woff;
+        sw[j] = pair_of<BF16>(r.inter ? __byte_perm(wb[j], wb[j], 0x1032) : wb[j]);
+        sw[j].x += r.woff, sw[j].y += r.woff;
+      }
+    }
+    const bool beyond = turns && r.rot > 0 && live && angle >= r.n_positions;
+    if (beyond) nan_pos = __uint_as_float(0x7FFFFFFFu);
+    if (rotated && live && !beyond) {
+      // a pair of the table is (cos, sin) of one angle
       const float* tab = r.table + (int64_t)angle * r.rot;
       if (r.inter) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(tab + lane * 8));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(tab + lane * 8) + 1);
-        cs[0] = a.x, sn[0] = a.y, cs[1] = a.z, sn[1] = a.w, cs[2] = b.x, sn[2] = b.y, cs[3] = b.z, sn[3] = b.w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 a = __ldg(reinterpret_cast<const float2*>(tab + lane * 8) + j);
+          cw[j].x *= a.x, cw[j].y *= a.x;
+          sw[j].x *= -a.y, sw[j].y *= a.y;
+        }
       } else {
         const bool first = lane < half8;
         const float4* p = reinterpret_cast<const float4*>(tab + (first ? lane : lane - half8) * 16);
-        sign = first ? -1.f : 1.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float4 a = __ldg(p + j);
-          cs[2 * j] = a.x, sn[2 * j] = sign * a.y, cs[2 * j + 1] = a.z, sn[2 * j + 1] = sign * a.w;
+          cw[j].x *= a.x, cw[j].y *= a.z;
+          sw[j].x *= first ? -a.y : a.y, sw[j].y *= first ? -a.w : a.w;
         }
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sw[j] = make_float2(0.f, 0.f);
     }
   }
-  if (NORM && lane < 2 * half8) partner = lane < half8 ? lane + half8 : lane - half8;
+  const bool to_cache = STORE && kind > 0;
+  const HeadDst dst = kind == 0 ? r.qo : r.ko;
+  uint16_t* to = dst.p + (int64_t)t * dst.ts + h0 * dst.hs + lane * 8;
 #pragma unroll
   for (int i = 0; i < kRowsPerUnit; ++i) {
-    const int h = s + i * r.slots;
-    if (i > 0 && i * r.slots >= H) break;  // uniform: no unit has an i-th row
+    if (i >= n) break;  // (the whole block)
     uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    if (NORM && __any_sync(0xffffffffu, h < r.nq + r.nk)) {
-      float f[8], ss = 0.f;
+    if (turns) {
+      float2 f[4], sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) unpack2<BF16>(w[j], f[2 * j], f[2 * j + 1]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+      for (int j = 0; j < 4; ++j) f[j] = pair_of<BF16>(w[j]), sum = fma2(f[j], f[j], sum);
+      float ss = sum.x + sum.y;
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float inv = rsqrtf(ss / (float)r.dim + r.eps) + nan_pos;
-      const uint16_t* wt = h < r.nq ? r.wq : r.wk;
-      uint4 wv = make_uint4(0, 0, 0, 0);
-      const bool weighted = wt != nullptr && in && h < r.nq + r.nk;
-      if (weighted) wv = __ldg(reinterpret_cast<const uint4*>(wt + lane * 8));
-      const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+      const float inv = rsqrtf(fmaf(ss, r.inv_dim, r.eps)) + nan_pos;
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float a, b;
-        unpack2<BF16>(ww[j], a, b);
-        f[2 * j] *= inv * (weighted ? a + r.woff : 1.f);
-        f[2 * j + 1] *= inv * (weighted ? b + r.woff : 1.f);
-      }
+      for (int j = 0; j < 4; ++j) f[j] = mul2(mul2(f[j], inv2), cw[j]);
       if (r.rot > 0) {
-        if (r.inter) {
-          if (lane < 2 * half8) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = f[2 * j], b = f[2 * j + 1];
-              f[2 * j] = a * cs[j] - b * sn[j];
-              f[2 * j + 1] = b * cs[j] + a * sn[j];
-            }
-          }
-        } else {
-          float g[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], partner, LPR);
-          if (sign != 0.f) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = f[j] * cs[j] + g[j] * sn[j];
-          }
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t o = r.inter ? __byte_perm(w[j], w[j], 0x1032) : __shfl_sync(0xffffffffu, w[j], partner, LPR);
+          f[j] = fma2(mul2(pair_of<BF16>(o), inv2), sw[j], f[j]);
         }
       }
-      if (!STORE || h < r.nq + r.nk) {  // a v row passes through
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack2<BF16>(f[2 * j], f[2 * j + 1]);
-      }
+      for (int j = 0; j < 4; ++j) w[j] = pack2<BF16>(f[j].x, f[j].y);
     }
-    if (!STORE || h < r.nq) {
-      if (live && in && h < H) {
-        const HeadDst& dst = h < r.nq ? r.qo : r.ko;
-        const int hh = h < r.nq ? h : h - r.nq;
-        *reinterpret_cast<uint4*>(dst.p + (int64_t)t * dst.ts + hh * dst.hs + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    if (STORE && __any_sync(0xffffffffu, h >= r.nq)) {
+    if (!to_cache) {
+      if (live && in) *reinterpret_cast<uint4*>(to + i * dst.hs) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
       constexpr int B = STORE ? BITS : 8, R = kv_row_bytes(LPR * 8, B);
-      float f[8];
       uint16_t scale;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) unpack2<BF16>(w[j], f[2 * j], f[2 * j + 1]);
-      const uint2 u = quantise8<B>(f, scale);  // the whole warp: shuffles
-      if (live && tile && h >= r.nq && h < H) {
-        const bool is_v = h >= r.nq + r.nk;
-        uint8_t* base = tile + (size_t)(h - r.nq - (is_v ? r.nk : 0)) * kv.head_bytes + (is_v ? kv_half_bytes(LPR * 8, B) : 0);
+      const uint2 u = quantise8<BF16, B>(w, scale);  // the whole warp: shuffles
+      if (live && tile) {
+        uint8_t* base = tile + (size_t)(h0 + i) * kv.head_bytes + (kind == 2 ? kv_half_bytes(LPR * 8, B) : 0);
         const int turn = kv_turn(row) & (R / 16 - 1);
         if (B == 8)
           *reinterpret_cast<uint2*>(base + row * R + (((lane >> 1) ^ turn) << 4) + (lane & 1) * 8) = u;
@@ -331,18 +372,22 @@ HeadDst dst_of(const moe_heads_t* h) {
 
 template <int LPR, bool NORM, int BITS>
 moe_status_t launch_rows(RowArgs r, const KvArgs& kv, bool bf16, cudaStream_t st) {
-  const int H = r.nq + r.nk + (BITS ? r.nk : 0);
+  const int64_t H = (int64_t)r.nq + r.nk + (BITS ? r.nk : 0);
   // One row a group while that fills the GPU at most once over, so that a
   // small call's rows all run side by side; several rows of a token a group
   // above that, which reuses the token's angles and page.
+  if (H > 65535) return MOE_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)r.n_tokens * H;
-  r.slots = rows * LPR <= 152 * 2048 ? H : (H + kRowsPerUnit - 1) / kRowsPerUnit;
-  if ((int64_t)r.n_tokens * r.slots > INT32_MAX - kRowThreads) return MOE_ERR_INVALID_ARG;
-  const int64_t blocks = ((int64_t)r.n_tokens * r.slots * LPR + kRowThreads - 1) / kRowThreads;
+  r.per = rows * LPR <= 152 * 2048 ? 1 : kRowsPerUnit;
+  r.q_slots = (r.nq + r.per - 1) / r.per;
+  r.k_slots = (r.nk + r.per - 1) / r.per;
+  r.inv_dim = 1.f / (float)r.dim;
+  const unsigned slots = (unsigned)(r.q_slots + (BITS ? 2 : 1) * r.k_slots);
+  const dim3 blocks((unsigned)(((int64_t)r.n_tokens * LPR + kRowThreads - 1) / kRowThreads), slots);
   if (bf16)
-    head_rows_kernel<LPR, true, NORM, BITS><<<(int)blocks, kRowThreads, 0, st>>>(r, kv);
+    head_rows_kernel<LPR, true, NORM, BITS><<<blocks, kRowThreads, 0, st>>>(r, kv);
   else
-    head_rows_kernel<LPR, false, NORM, BITS><<<(int)blocks, kRowThreads, 0, st>>>(r, kv);
+    head_rows_kernel<LPR, false, NORM, BITS><<<blocks, kRowThreads, 0, st>>>(r, kv);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -206,12 +206,12 @@ def shared_case(bits, dim, hkv, group, share, seqs, seed=0):
     return cache, batch, table, q, kv, news, lens
 
 
-@pytest.mark.parametrize("bits,dim,group,share,seqs", [(8, 128, 2, 1024, 170), (4, 256, 2, 1024, 170), (8, 64, 3, 1920, 180),
-                                                       (4, 128, 5, 1984, 160), (8, 256, 1, 576, 160), (4, 64, 2, 1920, 330)])
+@pytest.mark.parametrize("bits,dim,group,share,seqs", [(8, 128, 2, 1024, 280), (4, 256, 2, 1024, 280), (8, 64, 3, 1920, 180),
+                                                       (4, 128, 5, 1984, 160), (8, 256, 1, 576, 500), (4, 64, 2, 1920, 330)])
 def test_shared_prefix_read_once(bits, dim, group, share, seqs):
-    """Enough reads spared for a pass of its own: seqs * share * 4 heads of more than 160 MB."""
+    """Enough reads spared for a pass of its own: a million keys, counted a kv head."""
     import torch
-    assert (seqs * 0.9) * share * 4 * (dim * bits / 4 + dim / 8) > 160e6
+    assert (seqs * 0.9) * share * 4 > 1e6
     cache, batch, _, q, kv, news, lens = shared_case(bits, dim, 4, group, share, seqs)
     lse = torch.zeros(q.shape[:2], device="cuda")
     out = cache.attend(q, batch, lse=lse, shared_tokens=share)
@@ -224,7 +224,7 @@ def test_shared_prefix_captured_and_with_a_bad_page():
     import torch
     from quantized_expert_ffn_gemv_gb300 import moe
     share = 1024
-    cache, batch, table, q, _, news, lens = shared_case(8, 128, 4, 2, share, 170)
+    cache, batch, table, q, _, news, lens = shared_case(8, 128, 4, 2, share, 280)
     eager = cache.attend(q, batch, shared_tokens=share)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
