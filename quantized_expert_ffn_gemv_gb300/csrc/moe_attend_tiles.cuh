@@ -7,8 +7,11 @@
 //   dequantise (4 + 4)  integer times scale, rounded to fp16 once, into
 //                       128-byte swizzled stages: four warps K as the K-major,
 //                       four V, which has the same rows, as the MN-major operand
-//   issue (1)           S = Q K^T (tcgen05.mma, fp32 in tensor memory, two
-//                       buffers a row tile), O += P V with P read from tensor memory
+//   issue (1 a tile)    S = Q K^T (tcgen05.mma, fp32 in tensor memory, two
+//                       buffers a row tile), O += P V with P read from tensor
+//                       memory, and so is Q where it fits (heads of 64 and 256):
+//                       products of 64 keys with both operands in shared
+//                       memory take 48 cycles, with Q in tensor memory 32
 //   softmax (4 a tile)  a thread a row: maximum, exponentials, sum; P goes
 //                       back into S's columns as fp16 (times 2^8, as in
 //                       attend_rows_kernel).  O is rescaled in tensor memory
@@ -16,9 +19,9 @@
 //                       last time, which keeps P below fp16's largest.
 // Registers move from the dequantising warps to the softmax (setmaxnreg).
 // The two row tiles share the dequantised keys and keep the tensor core busy
-// while the other's softmax runs.  Per 64 keys (heads of 128) the tensor core
-// needs about 1,000 cycles, the four schedulers 300 issue slots for the
-// dequantisation and 800 for the softmax: they bound it together.
+// while the other's softmax runs.  A step of 64 keys (heads of 128, 256 rows)
+// is 24 products, 1,240 cycles of the tensor core; one warp that issued both
+// tiles' products, with its waits and elections, took 2,500.
 //
 // The line of work is measured in keys, causal limits included, so that all
 // parts cost the same: row tile rt of a sequence costs kSegmentKeys + the keys
@@ -48,16 +51,16 @@ struct TilesPlan {
   static constexpr int kHalf = kv_half_bytes(D, BITS);
   static constexpr int kHalves = D == 256 && BITS == 8 ? 1 : 2;  // half tiles of a ring entry
   static constexpr int kEntry = kHalves * kHalf;
-  static constexpr int kEntries = 3;                              // of either ring
+  static constexpr int kEntries = D == 256 ? 5 : 3;               // of either ring
   static constexpr int kStage = kKeys * D * 2;
-  static constexpr int kVStages = D == 256 ? 1 : 2;
-  static constexpr int kQ = 128 * D * 2;
+  static constexpr bool kQTmem = D != 128;  // queries in tensor memory
+  static constexpr int kQ = kQTmem ? 0 : 128 * D * 2;
   static constexpr int kOffK = NRT * kQ;
   static constexpr int kOffV = kOffK + 2 * kStage;
-  static constexpr int kOffRaw = kOffV + kVStages * kStage;
+  static constexpr int kOffRaw = kOffV + 2 * kStage;
   static constexpr int kOffBar = (kOffRaw + 2 * kEntries * kEntry + 15) & ~15;
   // barriers: raw full and empty of either ring, K full and empty, V full and empty, Q full, S full, P full, O done
-  static constexpr int kBars = 4 * kEntries + 4 + 2 * kVStages + NRT * 6;
+  static constexpr int kBars = 4 * kEntries + 8 + NRT * 6;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64;
   static constexpr int kSoftWarps = 4 * NRT;
@@ -67,26 +70,39 @@ struct TilesPlan {
   static constexpr int kSoftRegs = NRT == 2 ? 152 : 208, kDeqRegs = NRT == 2 ? 64 : 104, kRestRegs = NRT == 2 ? 48 : 96;
   static_assert(kSoftWarps * kSoftRegs + 2 * kDeqWarps * kDeqRegs + 4 * kRestRegs <= kThreads / 32 * kLaunchRegs, "registers");
   static constexpr int kTmemO = NRT * 2 * kKeys;  // S buffers first, then O
-  static constexpr int kTmemCols = kTmemO + NRT * D <= 256 ? 256 : 512;
+  static constexpr int kTmemQ = kTmemO + NRT * D;
+  static constexpr int kTmemCols = 512;
   static_assert(kSmem <= 232448, "shared memory of an SM");
-  static_assert(kTmemO + NRT * D <= 512, "tensor memory");
+  static_assert(kTmemQ + (kQTmem ? NRT * D / 2 : 0) <= kTmemCols, "tensor memory");
 };
 
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// The whole warp calls these with the same operands and one lane issues: under
-// a branch of one lane the operands' way into uniform registers costs more
-// than the product does.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-               "l"(a), "l"(b), "r"(idesc), "r"(acc)
-               : "memory");
+// Four products, K = 64, the first adding to D if acc.  The whole warp calls
+// these with the same operands and one lane issues: under a branch of one
+// lane the operands' way into uniform registers costs more than the product
+// does, and so does an election for each.
+__device__ __forceinline__ void tc_mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, t, e;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, %3, %3;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
 }
-// A from tensor memory: two fp16 of a row in each 32-bit column.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-               "r"(a), "l"(b), "r"(idesc), "r"(acc)
-               : "memory");
+// A from tensor memory: two fp16 of a row in each 32-bit column.  B advances by B_STEP 16-byte units.
+template <int B_STEP>
+__device__ __forceinline__ void tc_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, t, e;\n .reg .b32 a;\n .reg .b64 b;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, %3, %3;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n add.s32 a, %1, 8;\n add.s64 b, %2, %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n add.s32 a, %1, 16;\n add.s64 b, %2, 2 * %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n add.s32 a, %1, 24;\n add.s64 b, %2, 3 * %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(B_STEP)
+      : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
@@ -292,7 +308,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
   auto bar = [&](int i) { return sm + P::kOffBar + 8 * i; };
   constexpr int kRawFull = 0, kRawEmpty = 2 * P::kEntries, kKFull = 4 * P::kEntries,  // raw: K's ring, then V's
                 kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
-                kVEmpty = kVFull + P::kVStages, kQFull = kVEmpty + P::kVStages, kSFull = kQFull + NRT, kPFull = kSFull + 2 * NRT,
+                kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kSFull = kQFull + NRT, kPFull = kSFull + 2 * NRT,
                 kODone = kPFull + 2 * NRT;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P::kOffMisc);
   int* s_bad = reinterpret_cast<int*>(smem + P::kOffMisc + 16);  // [8], by piece: position of the first bad page or non-finite V
@@ -307,11 +323,11 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kKFull + i), kDeqWarps);
-      mbar_init(bar(kKEmpty + i), 1);
+      mbar_init(bar(kKEmpty + i), NRT);
     }
-    for (int i = 0; i < P::kVStages; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kVFull + i), kDeqWarps);
-      mbar_init(bar(kVEmpty + i), 1);
+      mbar_init(bar(kVEmpty + i), NRT);
     }
     for (int i = 0; i < NRT; ++i) {
       mbar_init(bar(kQFull + i), 4);
@@ -324,7 +340,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     fence_mbar_init();
   }
   if (tid < 8) s_bad[tid] = INT32_MAX;
-  constexpr int kIssueWarp = P::kSoftWarps + 2 * kDeqWarps, kLoadWarp = kIssueWarp + 1;
+  constexpr int kIssueWarp = P::kSoftWarps + 2 * kDeqWarps, kLoadWarp = kIssueWarp + 1;  // (the second row tile's products: kIssueWarp + 2)
   if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "n"(P::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -430,50 +446,53 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
           if (++entry == P::kEntries) entry = 0, phase ^= 1;
         }
       }
-    } else if (warp == kIssueWarp) {
-      // ---------------------------------------------------------------- issue
-      {
-        constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
-        uint32_t step = 0, own0 = 0, own1 = 0, pieces0 = 0, pieces1 = 0;  // steps over all pieces; either row tile's steps and pieces
-        while (walk.next(a, t, p)) {
-          const int n = p.t1 - p.t0, tiles = min(NRT, (p.rows + 127) / 128);  // row tiles that hold rows
-          mbar_wait(bar(kQFull), pieces0++ & 1, ok);
-          if (tiles > 1) mbar_wait(bar(kQFull + 1), pieces1++ & 1, ok);
-          for (int j = 0; j <= n; ++j) {
-            const uint32_t g = step + j, kst = g & 1;
-            if (j < n) mbar_wait(bar(kKFull + kst), (g >> 1) & 1, ok);
-            tc_after();
-#pragma unroll 1
-            for (int i = 0; i < tiles; ++i) {  // (unrolled, the operands would not fit the uniform registers)
-              const uint32_t own = i ? own1 : own0;
-              if (j < n) {
-                const uint32_t sb = (own + j) & 1;
-                const uint32_t q = sm + i * P::kQ, k = sm + P::kOffK + kst * P::kStage, d = tmem + (2 * i + sb) * kKeys;
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x)
-                  tc_mma(d, desc_k(q + (x >> 2) * (128 * 128) + (x & 3) * 32), desc_k(k + (x >> 2) * (kKeys * 128) + (x & 3) * 32),
-                         kIdS, x > 0);
-                tc_commit(bar(kSFull + 2 * i + sb));
-                if (i == tiles - 1) tc_commit(bar(kKEmpty + kst));
-              }
-              if (j > 0) {
-                const uint32_t f = g - 1, vst = f % P::kVStages, of = own + j - 1, pb = of & 1;
-                mbar_wait(bar(kPFull + 2 * i + pb), (of >> 1) & 1, ok);
-                if (i == 0) mbar_wait(bar(kVFull + vst), (f / P::kVStages) & 1, ok);
-                tc_after();
-                const uint32_t v = sm + P::kOffV + vst * P::kStage, s = tmem + (2 * i + pb) * kKeys, o = tmem + P::kTmemO + i * D;
-#pragma unroll
-                for (int x = 0; x < kKeys / 16; ++x)
-                  tc_mma_ts(o, s + x * 8, desc_mn(v + x * 2048, kKeys * 128), kIdO, j > 1 || x > 0);
-                tc_commit(bar(kODone + i));
-                if (i == tiles - 1) tc_commit(bar(kVEmpty + vst));
-              }
-            }
+    } else if (warp == kIssueWarp || (NRT == 2 && warp == kIssueWarp + 2)) {
+      // ---------------------------------------------------------------- issue, a warp a row tile
+      constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
+      const int i = warp == kIssueWarp ? 0 : 1;
+      uint32_t step = 0, own = 0, pieces = 0;  // steps over all pieces; the row tile's steps and pieces
+      while (walk.next(a, t, p)) {
+        const int n = p.t1 - p.t0;
+        if (i * 128 >= p.rows) {  // no rows in the tile: the stages pass by
+          for (int j = 0; j < n; ++j, ++step) {
+            mbar_wait(bar(kKFull + (step & 1)), (step >> 1) & 1, ok);
+            if (lane == 0) mbar_arrive(bar(kKEmpty + (step & 1)));
+            mbar_wait(bar(kVFull + (step & 1)), (step >> 1) & 1, ok);
+            if (lane == 0) mbar_arrive(bar(kVEmpty + (step & 1)));
           }
-          step += n;
-          own0 += n;
-          if (tiles > 1) own1 += n;
+          continue;
         }
+        mbar_wait(bar(kQFull + i), pieces++ & 1, ok);
+        for (int j = 0; j <= n; ++j) {
+          if (j < n) {
+            const uint32_t st = (step + j) & 1, sb = (own + j) & 1;
+            const uint32_t k = sm + P::kOffK + st * P::kStage, d = tmem + (2 * i + sb) * kKeys;
+            mbar_wait(bar(kKFull + st), ((step + j) >> 1) & 1, ok);
+            tc_after();
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+              if (P::kQTmem)
+                tc_mma4_ts<2>(d, tmem + P::kTmemQ + i * (D / 2) + x * 32, desc_k(k + x * (kKeys * 128)), kIdS, x > 0);
+              else
+                tc_mma4(d, desc_k(sm + i * P::kQ + x * (128 * 128)), desc_k(k + x * (kKeys * 128)), kIdS, x > 0);
+            }
+            tc_commit(bar(kSFull + 2 * i + sb));
+            tc_commit(bar(kKEmpty + st));
+          }
+          if (j > 0) {
+            const uint32_t f = step + j - 1, st = f & 1, of = own + j - 1, pb = of & 1;
+            mbar_wait(bar(kVFull + st), (f >> 1) & 1, ok);
+            mbar_wait(bar(kPFull + 2 * i + pb), (of >> 1) & 1, ok);
+            tc_after();
+            static_assert(kKeys == 64, "one call");
+            tc_mma4_ts<2048 / 16>(tmem + P::kTmemO + i * D, tmem + (2 * i + pb) * kKeys, desc_mn(sm + P::kOffV + st * P::kStage, kKeys * 128), kIdO,
+                                  j > 1);
+            tc_commit(bar(kODone + i));
+            tc_commit(bar(kVEmpty + st));
+          }
+        }
+        step += n;
+        own += n;
       }
     }
   } else if (warp >= P::kSoftWarps) {
@@ -481,7 +500,6 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     give_registers<P::kDeqRegs>();
     const int dt = tid & 127;
     const bool v = warp >= P::kSoftWarps + kDeqWarps;  // which stream
-    const uint32_t stages = v ? P::kVStages : 2;
     uint32_t magic = 0x64006400u;
     asm volatile("" : "+r"(magic));
     int entry = 0;
@@ -490,8 +508,8 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
       if (v && dt == 0) s_bad[(piece + 4) & 7] = INT32_MAX;  // (no warp is more than three pieces from another)
       const int lim = p.lim;
       for (int j = p.t0; j < p.t1; ++j, ++step) {
-        const uint32_t st = step % stages;
-        mbar_wait(v ? bar(kVEmpty + st) : bar(kKEmpty + st), ((step / stages) & 1) ^ 1, ok);
+        const uint32_t st = step & 1;
+        mbar_wait(v ? bar(kVEmpty + st) : bar(kKEmpty + st), ((step >> 1) & 1) ^ 1, ok);
 #pragma unroll
         for (int h = 0; h < 2; h += P::kHalves) {
           const int pos0 = j * kKeys + h * kKvTile, e = (v ? P::kEntries : 0) + entry;
@@ -545,18 +563,32 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
         const float down = query_factor(t.scale_log2, e);
         c = score_factor(t.scale_log2, e);
         const uint32_t dst = sm + i * P::kQ + row * 128;
-#pragma unroll 4
-        for (int x = 0; x < D / 8; ++x) {
-          const uint4 w = live ? src[x] : make_uint4(0, 0, 0, 0);
-          float f[8];
-          unpack2<BF16>(w.x, f[0], f[1]), unpack2<BF16>(w.y, f[2], f[3]), unpack2<BF16>(w.z, f[4], f[5]), unpack2<BF16>(w.w, f[6], f[7]);
-          uint32_t h[4];
+#pragma unroll 1
+        for (int x0 = 0; x0 < D / 8; x0 += 4) {
+          uint32_t h[16];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            h[y] = BITS == 8 ? pack2<false>(f[2 * y] * down, f[2 * y + 1] * down) : pack2<false>(f[y] * down, f[y + 4] * down);
-          sts128(dst + (x >> 3) * (128 * 128) + (((x & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+          for (int x = 0; x < 4; ++x) {
+            const uint4 w = live ? src[x0 + x] : make_uint4(0, 0, 0, 0);
+            float f[8];
+            unpack2<BF16>(w.x, f[0], f[1]), unpack2<BF16>(w.y, f[2], f[3]), unpack2<BF16>(w.z, f[4], f[5]), unpack2<BF16>(w.w, f[6], f[7]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              h[4 * x + y] = BITS == 8 ? pack2<false>(f[2 * y] * down, f[2 * y + 1] * down) : pack2<false>(f[y] * down, f[y + 4] * down);
+          }
+          if (P::kQTmem) {
+            tc_st16(tmem + P::kTmemQ + i * (D / 2) + lanes + x0 * 4, h);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              sts128(dst + ((x0 + x) >> 3) * (128 * 128) + ((((x0 + x) & 7) ^ (row & 7)) << 4), h[4 * x], h[4 * x + 1], h[4 * x + 2], h[4 * x + 3]);
+          }
         }
-        fence_async_shared();
+        if (P::kQTmem) {
+          tc_wait_st();
+          tc_before();
+        } else {
+          fence_async_shared();
+        }
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(bar(kQFull + i));
