@@ -51,7 +51,7 @@ struct TilesPlan {
   static constexpr int kHalf = kv_half_bytes(D, BITS);
   static constexpr int kHalves = D == 256 && BITS == 8 ? 1 : 2;  // half tiles of a ring entry
   static constexpr int kEntry = kHalves * kHalf;
-  static constexpr int kEntries = D == 256 ? 5 : 3;               // of either ring
+  static constexpr int kEntries = D == 256 ? 4 : 3;               // of either ring
   static constexpr int kStage = kKeys * D * 2;
   static constexpr bool kQTmem = D != 128;  // queries in tensor memory
   static constexpr int kQ = kQTmem ? 0 : 128 * D * 2;
