@@ -213,7 +213,7 @@ MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const moe_kv_bat
  *          exceeds u times the kept sum
  * temperature <= 0 is greedy: the first of the order.  A NaN parameter is
  * taken as off (temperature: greedy).  Weights are evaluated to about 2^-31
- * relative (2^-24 for a 16-bit logit nearer zero than 2^-13 of the maximum) and summed as integers (units of 2^-45 of the largest), so results
+ * relative and summed as integers (units of 2^-45 of the largest), so results
  * do not depend on the order of execution.  Temperatures are clamped to
  * 1e-30..1e30.  A maximum of +infinity: equal weight for every infinite
  * logit, none for the rest.  A row without a number above -infinity has no

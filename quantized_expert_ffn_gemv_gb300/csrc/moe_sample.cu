@@ -5,8 +5,7 @@
 // for a single row it is the chain of cluster barriers.
 //
 // Weights w = 2^-y, y = (max - z) log2(e) / T, are evaluated to about 2^-31
-// relative (float pairs for y, a 512-entry table and a cubic for the rest;
-// 2^-24 for a 16-bit logit nearer zero than 2^-13 of the maximum)
+// relative (float pairs for y, a 512-entry table and a cubic for the rest)
 // and summed as integers in units of 2^-45: integer sums have no order, so
 // any split of the work gives the same bits, and the sums that top-p, min-p
 // and the draw compare are exact.  Conversions go through the float's
@@ -97,9 +96,7 @@ __device__ __forceinline__ float y_of(float z, float m, const Rate& c) { return 
 __device__ __forceinline__ int bin_of(float y) { return min(__float_as_int(fmaf(y, (float)kPerOctave, kMagic)) - kMagicBits, kBins - 1); }
 
 // w = W 2^-(31 + s - 1), W in 2^30 .. 2^31.  From 64 octaves on W is
-// anything and s at least 64, which to_units makes 0.  EXACT: m - z is taken
-// with its rounding error; 16-bit logits need it only below 2^-13 of m.
-template <bool EXACT>
+// anything and s at least 64, which to_units makes 0.
 __device__ __forceinline__ uint32_t weight31(float z, float m, const Rate& c, const float2* tab, int& s) {
   const float x = m - z;
   const float kf = fmaf(fminf(x * c.h, 100.f), (float)kTable, kMagic);  // (y_of's product)
@@ -107,10 +104,8 @@ __device__ __forceinline__ uint32_t weight31(float z, float m, const Rate& c, co
   // r = y - round(512 y) / 512, small, from y = (x + xl) (c.h + c.l)
   float r = fmaf(x, c.h, (kf - kMagic) * (-1.f / kTable));
   r = fmaf(x, c.l, r);
-  if (EXACT) {
-    const float bb = x - m;
-    r = fmaf((m - (x - bb)) + (-z - bb), c.h, r);  // m - z = x + that
-  }
+  const float bb = x - m;
+  r = fmaf((m - (x - bb)) + (-z - bb), c.h, r);  // m - z = x + that
   // 2^-r - 1 by its series: |r| < 2^-10
   const float p = r * fmaf(r, fmaf(r, -0.0555041087f, 0.2402265070f), -0.6931471806f);
   const float2 t = tab[k & (kTable - 1)];  // t.x in 1/2 .. 1
@@ -128,10 +123,9 @@ __device__ __forceinline__ uint64_t to_units(uint32_t W, int s) {
   asm("shr.u32 %0, %1, %2;" : "=r"(w) : "r"(W + (half >> 1)), "r"(down));
   return (uint64_t)w * mul;
 }
-template <bool EXACT>
 __device__ __forceinline__ uint64_t weight(float z, float m, const Rate& c, const float2* tab) {
   int s;
-  const uint32_t W = weight31<EXACT>(z, m, c, tab, s);
+  const uint32_t W = weight31(z, m, c, tab, s);
   return to_units(W, s);
 }
 
@@ -320,12 +314,11 @@ __device__ __forceinline__ uint64_t sum_before(const Shared& s, int n, int share
 }
 // Ranks the list's n <= kList elements.  500 of them take 18 us by comparing
 // all with all and 3 by sorting; 50 take 2 and 4.
-template <bool EXACT>
 __device__ __forceinline__ Ranked rank_list(Shared& s, const Slice& v, int n) {
   const int tid = threadIdx.x;
   Ranked r{tid < n ? s.list[tid] : 0, 0, 0, (uint32_t)tid};
   if (n > kDirect) r.e = sort_values(s, r.e, 1 << (32 - __clz(n - 1)));
-  if (tid < n) r.w = weight<EXACT>(logit_of(key_in(r.e)), v.m, v.c, s.pow2);
+  if (tid < n) r.w = weight(logit_of(key_in(r.e)), v.m, v.c, s.pow2);
   if (n > kDirect) {
     uint32_t none = 0;
     r.front = r.w;
@@ -345,10 +338,9 @@ __device__ __forceinline__ Ranked rank_list(Shared& s, const Slice& v, int n) {
 // The first CTA alone: every element that top-k and top-p can keep is in the
 // list, n of them; cut them, and draw the token.  target: the mass that top-p
 // asks for, or 0: its share of what top-k keeps of the list.
-template <bool EXACT>
 __device__ void draw_from_list(Shared& s, const Slice& v, int n, uint64_t target) {
   const int tid = threadIdx.x;
-  const Ranked r = rank_list<EXACT>(s, v, n);
+  const Ranked r = rank_list(s, v, n);
   uint64_t w = v.k > 0 && r.place >= v.k ? 0 : r.w;
   if (v.p < 1.f) {
     // front < sum * p  <=>  front < ceil(sum * p)
@@ -434,7 +426,6 @@ __device__ __forceinline__ void each_of(const Slice& v, int first, int end, P pr
 // reaches top-p of it all.  The whole cluster calls it.  True: the token is
 // drawn.  Otherwise the cut is in the first CTA's Shared::cut until the
 // caller's next cluster barrier.
-template <bool EXACT>
 __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, const Slice& v, const Cut limit, bool limited,
                          bool by_mass) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -472,7 +463,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       if (by_mass) {
         if (bin == kBins - 1) return;
         int sh;
-        uint32_t W = weight31<EXACT>(z, v.m, v.c, s.pow2, sh);
+        uint32_t W = weight31(z, v.m, v.c, s.pow2, sh);
         W >>= sh - (level == 0 ? bin / kPerOctave : octave);  // relative to the bin's octave, which a weight is at most one below
         atomicAdd(&s.h.hi[bin], W >> 16);
         atomicAdd(&s.h.lo[bin], W & 0xFFFFu);
@@ -624,9 +615,9 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
           }
           __syncthreads();
           if (fits) {
-            draw_from_list<EXACT>(s, v, to, by_mass ? target : 0);
+            draw_from_list(s, v, to, by_mass ? target : 0);
           } else {
-            const Ranked r = rank_list<EXACT>(s, v, to);
+            const Ranked r = rank_list(s, v, to);
             // the need-th; or the one whose weight takes the mass to the target: the
             // first or the last where rounding has put the target before or behind them
             const uint64_t front = before + r.front;
@@ -650,7 +641,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
       const uint32_t k = top_key;
       uint32_t want = need;
       if (by_mass) {
-        const uint64_t w = weight<EXACT>(logit_of(k), v.m, v.c, s.pow2), more = target > before ? target - before : 1;
+        const uint64_t w = weight(logit_of(k), v.m, v.c, s.pow2), more = target > before ? target - before : 1;
         want = w ? (uint32_t)min((more + w - 1) / w, (uint64_t)UINT32_MAX) : UINT32_MAX;
       }
       const float* z = reinterpret_cast<const float*>(v.z);
@@ -781,7 +772,6 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   const int k0 = a.top_k ? a.top_k[row] : 0;
   const float p0 = a.top_p ? a.top_p[row] : 1.f, q0 = a.min_p ? a.min_p[row] : 0.f;
   const float u0 = a.u[row];
-  constexpr bool EXACT = sizeof(T) == 4;
 
   float wtop = top;
 #pragma unroll
@@ -837,7 +827,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   bool limited = false;
   for (int step = 0; step < 2; ++step) {
     if (step == 0 ? !top_k : !top_p) continue;
-    if (find_cut<EXACT>(cluster, s, s0, v, cut, limited, step == 1)) return;  // drawn
+    if (find_cut(cluster, s, s0, v, cut, limited, step == 1)) return;  // drawn
     cut = s0->cut;
     limited = true;
     cluster.sync();
@@ -847,7 +837,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   const float z_cut = limited ? logit_of(cut.key) : -INFINITY;
   auto is_kept = [&](float zi, uint32_t idx) { return zi >= z_cut && (!limited || kept(key_of(zi), idx, cut)); };
   auto weigh = [&](float zi) -> uint64_t {
-    const uint64_t w = weight<EXACT>(zi, m, v.c, s.pow2);
+    const uint64_t w = weight(zi, m, v.c, s.pow2);
     return w >= least ? w : 0;
   };
   auto load4 = [&](int i) { return i < hi ? v.z[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); };
