@@ -17,6 +17,10 @@
 //                       attend_rows_kernel).  O is rescaled in tensor memory
 //                       only when a maximum grew by more than 2^7 since the
 //                       last time, which keeps P below fp16's largest.
+// An fp16 K has 11 bits where integer times scale has up to 19.  That is
+// within what outputs of bf16 show; with fp16 activations it was the largest
+// error (5.4e-4 of the output, of 2.1e-4 for its own rounding), so there the
+// rest of K, exact in fp16 too, is a second operand of S.
 // Registers move from the dequantising warps to the softmax (setmaxnreg).
 // The two row tiles share the dequantised keys and keep the tensor core busy
 // while the other's softmax runs.  A step of 64 keys (heads of 128, 256 rows)
@@ -44,27 +48,28 @@ constexpr int kSegmentKeys = 512;   // what a segment costs beside its keys, in 
 constexpr float kGrow = 7.f;        // log2 by which a maximum may outgrow its reference
 constexpr int kDeqWarps = 4;        // of either stream
 
-template <int D, int BITS>
+template <int D, int BITS, bool BF16>
 struct TilesPlan {
   static constexpr int NRT = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * NRT;
   static constexpr int kHalf = kv_half_bytes(D, BITS);
-  static constexpr int kHalves = D == 256 && BITS == 8 ? 1 : 2;  // half tiles of a ring entry
+  static constexpr bool kRest = !BF16;                           // K's rest, too
+  static constexpr int kHalves = D == 256 && (BITS == 8 || kRest) ? 1 : 2;  // half tiles of a ring entry
   static constexpr int kEntry = kHalves * kHalf;
-  static constexpr int kEntries = D == 256 ? 4 : 3;               // of either ring
-  static constexpr int kStage = kKeys * D * 2;
+  static constexpr int kEntries = D == 256 ? (kRest ? (BITS == 8 ? 2 : 3) : 4) : 3;  // of either ring
+  static constexpr int kStage = kKeys * D * 2, kKStage = kStage * (kRest ? 2 : 1);
   static constexpr bool kQTmem = D != 128;  // queries in tensor memory
   static constexpr int kQ = kQTmem ? 0 : 128 * D * 2;
   static constexpr int kOffK = NRT * kQ;
-  static constexpr int kOffV = kOffK + 2 * kStage;
+  static constexpr int kOffV = kOffK + 2 * kKStage;
   static constexpr int kOffRaw = kOffV + 2 * kStage;
   static constexpr int kOffBar = (kOffRaw + 2 * kEntries * kEntry + 15) & ~15;
   // barriers: raw full and empty of either ring, K full and empty, V full and empty, Q full, S full, P full, O done
   static constexpr int kBars = 4 * kEntries + 8 + NRT * 6;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
-  static constexpr int kSmem = kOffMisc + 64;
   static constexpr int kSoftWarps = 4 * NRT;
   static constexpr int kThreads = 32 * (kSoftWarps + 2 * kDeqWarps + 4);
+  static constexpr int kSmem = kOffMisc + 72 + kThreads / 32 * 8;
   // registers of the roles' warpgroups: together no more than the launch's
   static constexpr int kLaunchRegs = NRT == 2 ? 96 : 128;
   static constexpr int kSoftRegs = NRT == 2 ? 152 : 208, kDeqRegs = NRT == 2 ? 64 : 104, kRestRegs = NRT == 2 ? 48 : 96;
@@ -229,8 +234,9 @@ struct Walk {
 // The integers times scales of an entry's HALVES * 32 keys into rows key_base
 // .. of a stage, all loads first.  V: keys from lim on (of the first key) are
 // seen by no row and become 0, and so do blocks of non-finite scale; the
-// first such key's position goes to `bad`.
-template <int D, int BITS, int HALVES>
+// first such key's position goes to `bad`.  REST, K: what the rounding left
+// goes a stage further.
+template <int D, int BITS, int HALVES, bool REST>
 __device__ __forceinline__ void dequantise(uint32_t raw, uint32_t stage, int key_base, int tid, bool is_v, int lim, int pos0, int* bad,
                                            uint32_t magic) {
   constexpr int R = kv_row_bytes(D, BITS), UPR = R / 16, EPU = 128 / BITS;  // 16-byte units a row, elements a unit
@@ -268,22 +274,31 @@ __device__ __forceinline__ void dequantise(uint32_t raw, uint32_t stage, int key
       const uint32_t w[4] = {w4[h][n].x, w4[h][n].y, w4[h][n].z, w4[h][n].w};
 #pragma unroll
       for (int i = 0; i < EPU / 8; ++i) {
-        uint32_t x[4];
+        uint32_t x[4];  // the integers
         if (BITS == 8) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            x[2 * j] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5150), 0x64806480u), sc);
-            x[2 * j + 1] = hmul2(hsub2(prmt(w[2 * i + j], magic, 0x5352), 0x64806480u), sc);
+            x[2 * j] = hsub2(prmt(w[2 * i + j], magic, 0x5150), 0x64806480u);
+            x[2 * j + 1] = hsub2(prmt(w[2 * i + j], magic, 0x5352), 0x64806480u);
           }
         } else {
           const uint32_t v = w[i], v8 = v >> 8;
-          x[0] = hmul2(hsub2(and_or<0x000F000Fu>(v, magic), 0x64086408u), sc);
-          x[1] = hmul2(hfma2(and_or<0x00F000F0u>(v, magic), 0x2C002C00u, 0xD480D480u), sc);
-          x[2] = hmul2(hsub2(and_or<0x000F000Fu>(v8, magic), 0x64086408u), sc);
-          x[3] = hmul2(hfma2(and_or<0x00F000F0u>(v8, magic), 0x2C002C00u, 0xD480D480u), sc);
+          x[0] = hsub2(and_or<0x000F000Fu>(v, magic), 0x64086408u);
+          x[1] = hfma2(and_or<0x00F000F0u>(v, magic), 0x2C002C00u, 0xD480D480u);
+          x[2] = hsub2(and_or<0x000F000Fu>(v8, magic), 0x64086408u);
+          x[3] = hfma2(and_or<0x00F000F0u>(v8, magic), 0x2C002C00u, 0xD480D480u);
         }
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = hmul2(x[j], sc);
         const int oc = c * (EPU / 8) + i;  // chunk of 8 elements
-        sts128(stage + (oc >> 3) * (kKeys * 128) + row * 128 + (((oc & 7) ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
+        const uint32_t to = stage + (oc >> 3) * (kKeys * 128) + row * 128 + (((oc & 7) ^ (row & 7)) << 4);
+        sts128(to, y[0], y[1], y[2], y[3]);
+        if (REST && !is_v) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = hfma2(x[j], sc, y[j] ^ 0x80008000u);
+          sts128(to + kKeys * D * 2, x[0], x[1], x[2], x[3]);
+        }
       }
     }
   }
@@ -299,8 +314,8 @@ __device__ __forceinline__ void take_registers() {
 }
 
 template <int D, int BITS, bool BF16>
-__global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tiles_kernel(const KvArgs a, const AttArgs t) {
-  using P = TilesPlan<D, BITS>;
+__global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) attend_tiles_kernel(const KvArgs a, const AttArgs t) {
+  using P = TilesPlan<D, BITS, BF16>;
   constexpr int NRT = P::NRT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sm = smem_u32(smem);
@@ -312,9 +327,10 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
                 kODone = kPFull + 2 * NRT;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P::kOffMisc);
   int* s_bad = reinterpret_cast<int*>(smem + P::kOffMisc + 16);  // [8], by piece: position of the first bad page or non-finite V
-  __shared__ long long s_sum[P::kThreads / 32];
-  __shared__ long long s_base;
-  __shared__ int s_b;
+  int& s_b = *reinterpret_cast<int*>(smem + P::kOffMisc + 48);
+  int* s_long = reinterpret_cast<int*>(smem + P::kOffMisc + 52);  // [2]
+  long long& s_base = *reinterpret_cast<long long*>(smem + P::kOffMisc + 64);
+  long long* s_sum = reinterpret_cast<long long*>(smem + P::kOffMisc + 72);  // [warps]
 
   if (tid == 0) {
     for (int i = 0; i < 2 * P::kEntries; ++i) {
@@ -358,7 +374,6 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
     if (s.len > longest) longest = s.len, longest_b = b;
     if (blockIdx.x == 0) flag_batch(a, b);
   }
-  __shared__ int s_long[2];
   if (t.shared) {  // the prefix is read through the longest sequence's row; there are no keys behind that one's length
     if (tid == 0) s_long[0] = s_long[1] = 0;
     __syncthreads();
@@ -466,15 +481,17 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
         for (int j = 0; j <= n; ++j) {
           if (j < n) {
             const uint32_t st = (step + j) & 1, sb = (own + j) & 1;
-            const uint32_t k = sm + P::kOffK + st * P::kStage, d = tmem + (2 * i + sb) * kKeys;
+            const uint32_t k = sm + P::kOffK + st * P::kKStage, d = tmem + (2 * i + sb) * kKeys;
             mbar_wait(bar(kKFull + st), ((step + j) >> 1) & 1, ok);
             tc_after();
 #pragma unroll
-            for (int x = 0; x < D / 64; ++x) {
+            for (int x = 0; x < D / 64 * (P::kRest ? 2 : 1); ++x) {  // (the rest lies a stage, D / 64 panels, further)
+              const uint64_t kd = desc_k(k + x * (kKeys * 128));
+              const int panel = x % (D / 64);
               if (P::kQTmem)
-                tc_mma4_ts<2>(d, tmem + P::kTmemQ + i * (D / 2) + x * 32, desc_k(k + x * (kKeys * 128)), kIdS, x > 0);
+                tc_mma4_ts<2>(d, tmem + P::kTmemQ + i * (D / 2) + panel * 32, kd, kIdS, x > 0);
               else
-                tc_mma4(d, desc_k(sm + i * P::kQ + x * (128 * 128)), desc_k(k + x * (kKeys * 128)), kIdS, x > 0);
+                tc_mma4(d, desc_k(sm + i * P::kQ + panel * (128 * 128)), kd, kIdS, x > 0);
             }
             tc_commit(bar(kSFull + 2 * i + sb));
             tc_commit(bar(kKEmpty + st));
@@ -514,8 +531,9 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
         for (int h = 0; h < 2; h += P::kHalves) {
           const int pos0 = j * kKeys + h * kKvTile, e = (v ? P::kEntries : 0) + entry;
           mbar_wait(bar(kRawFull + e), phase, ok);
-          dequantise<D, BITS, P::kHalves>(sm + P::kOffRaw + e * P::kEntry, sm + (v ? P::kOffV : P::kOffK) + st * P::kStage, h * kKvTile, dt,
-                                          v, lim - pos0, pos0, &s_bad[piece & 7], magic);
+          dequantise<D, BITS, P::kHalves, P::kRest>(sm + P::kOffRaw + e * P::kEntry,
+                                                    sm + (v ? P::kOffV + st * P::kStage : P::kOffK + st * P::kKStage), h * kKvTile, dt, v,
+                                                    lim - pos0, pos0, &s_bad[piece & 7], magic);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kRawEmpty + e));
           if (++entry == P::kEntries) entry = 0, phase ^= 1;
@@ -723,7 +741,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS>::kThreads), 1) attend_tile
 
 template <int D, int BITS, bool BF16>
 moe_status_t launch_tiles_kernel(const KvArgs& kv, const AttArgs& t, cudaStream_t st) {
-  using P = TilesPlan<D, BITS>;
+  using P = TilesPlan<D, BITS, BF16>;
   constexpr auto kernel = attend_tiles_kernel<D, BITS, BF16>;
   const moe_status_t ok = raise_smem<kernel>(P::kSmem);
   if (ok != MOE_OK) return ok;

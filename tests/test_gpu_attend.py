@@ -33,12 +33,13 @@ def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False, keys_rounded=F
     fp16's normal range, which are held times 2^8, by 2^-33 of the largest), a score is off by delta <= (D / 16 + 4) 2^-21 of the
     sum of its products' magnitudes (fp32 accumulation of D / 16 steps, two scalings, the exponential), which moves a term by
     2 delta relative; then half a step of the output's type.  With more than 64 rows a sequence (16 of heads of 256), or behind a
-    shared prefix, the keys, integer times scale, are rounded to fp16 too: delta grows by 2^-11 of the same sum."""
+    shared prefix, the keys, integer times scale, are rounded to fp16 too: delta grows by 2^-11 of the same sum; with fp16
+    activations by 2^-22, a rounding of what that left (and 2^-24 |q| where the rest is subnormal: keys here are not that small)."""
     import torch
     D, at = q.shape[2], 0
     group = q.shape[1] // kv[0][0].shape[1]
-    keys_rounded = 2.0 ** -11 if keys_rounded or max(news) * group > (16 if D == 256 else 64) else 0.0
     eps = torch.finfo(dt).eps
+    keys_rounded = (2.0 ** -11 if dt == torch.bfloat16 else 2.0 ** -22) if keys_rounded or max(news) * group > (16 if D == 256 else 64) else 0.0
     for (k, v), n, length in zip(kv, news, lens):
         if n == 0:
             continue
@@ -57,7 +58,7 @@ def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False, keys_rounded=F
             # of the norm: roundings are independent, uniform within half a step (1 / sqrt 3 of it).  Keys move a score by 2^-11 /
             # sqrt 3 of the root of its squared products' sum, which is the queries' size, 2; then P, V and the output
             step = 2.0 ** -11 / 3 ** 0.5
-            bound = ((2 * step) ** 2 * (keys_rounded > 0) + 2 * step ** 2 + (eps / 2) ** 2 / 3) ** 0.5
+            bound = ((2 * step) ** 2 * (keys_rounded > 2.0 ** -12) + 2 * step ** 2 + (eps / 2) ** 2 / 3) ** 0.5
             assert np.linalg.norm(err) <= 1.7 * bound * np.linalg.norm(want), np.linalg.norm(err) / np.linalg.norm(want)
         seen = np.isfinite(want_l)
         assert np.array_equal(seen, np.isfinite(got_l))
@@ -106,10 +107,11 @@ def test_several_tokens_and_none(bits, dim, page):
     run_case(bits, dim, page, 2, 3, [2, 0, 5, 1, 4, 9], [2, 10, 5, 64, 200, 37], pad=3)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("bits,dim,group,n,length", [(8, 128, 8, 90, 90), (4, 128, 2, 300, 517), (8, 64, 1, 130, 131), (4, 256, 4, 77, 400),
                                                      (8, 256, 2, 129, 129), (4, 64, 3, 200, 333), (8, 128, 1, 1, 2500)])
-def test_chunks(bits, dim, group, n, length):
-    run_case(bits, dim, 64, 2, group, [n, 1], [length, 3])
+def test_chunks(bits, dim, group, n, length, dtype):
+    run_case(bits, dim, 64, 2, group, [n, 1], [length, 3], dtype)
 
 
 def test_long_context_is_split_and_joined():
