@@ -177,8 +177,10 @@ MOE_API moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch
  *   out = softmax(scale * q k^T over positions <= the token's) v
  * Query head j reads kv head j / (n_q / n_kv_heads).  Scores, softmax
  * statistics and sums are fp32; probabilities and dequantised values enter
- * the products as fp16, and so do, with bf16 activations and many rows or
- * behind a shared prefix, dequantised keys.  lse (fp32 [n_tokens][n_q], or NULL): the natural
+ * the products as fp16, and so do, with many rows or behind a shared prefix,
+ * dequantised keys.  With fp16 activations only the values are rounded there,
+ * and otherwise only the probabilities: what the other roundings leave is a
+ * second operand.  lse (fp32 [n_tokens][n_q], or NULL): the natural
  * logarithm of the sum of exp(score).  A token of negative position sees
  * nothing: its out is 0 and its lse -infinity.  A row that meets a bad page
  * is NaN.  What lies in pages behind the position a row sees never reaches that row.

@@ -88,6 +88,18 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l) - kPShift) * 0.6931471805599453f;
 }
 
+// Probabilities and values enter the products rounded to fp16 once each.  With
+// fp16 outputs, whose own rounding is no larger, the two together made up to
+// 1.6 times its error: there a second product takes up the rest, of the values
+// in attend_rows_kernel, of keys and probabilities in attend_tiles_kernel,
+// whose shared memory has no room for a second V.
+// What rounding to fp16 left of a and b:
+__device__ __forceinline__ uint32_t rest_of(uint32_t held, float a, float b) {
+  float x, y;
+  unpack2<false>(held, x, y);
+  return pack2<false>(a - x, b - y);
+}
+
 // (v & mask) | bits in one instruction; `bits` has to be a register the
 // compiler cannot see through (two constants would take two instructions).
 template <uint32_t MASK>

@@ -121,10 +121,28 @@ __device__ __forceinline__ void score_tile(float (&s)[2][NT][4], uint32_t kb, ui
   }
 }
 
+// An m-tile of integers times scales, and with REST what rounding that to fp16
+// left (exact in fp16 too), against the probabilities.
+template <int NT, bool REST>
+__device__ __forceinline__ void value_product(float (&o)[NT][4], const uint32_t (&w)[4], const uint32_t (&sc)[2], const uint32_t (&p)[NT][2]) {
+  uint32_t a[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[j] = hmul2(w[j], sc[j >> 1]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mma_f16(o[n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
+  if (REST) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = hfma2(w[j], sc[j >> 1], a[j] ^ 0x80008000u);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma_f16(o[n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
+  }
+}
+
 // o += p v for 16 keys (step u of a tile).  edge: keys from lim on (within
 // the tile) are seen by no row and count as 0 whatever their bytes say, and so
-// do non-finite scales (the caller deals with the rows that see them).
-template <int D, int BITS, int NT>
+// do non-finite scales (the caller deals with the rows that see them).  REST: what
+// their rounding to fp16 left of integer times scale is a second operand.
+template <int D, int BITS, int NT, bool REST>
 __device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint32_t (&p)[NT][2], uint32_t vb, int u, int lane,
                                            bool edge, int lim, uint32_t magic) {
   constexpr int R = kv_row_bytes(D, BITS), NC = R / 16, RUN = D / 8;
@@ -168,13 +186,9 @@ __device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t x = prmt(v[0][w], v[1][w], h ? 0x7362 : 0x5140), y = prmt(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
-          uint32_t a[4];
-          a[0] = hmul2(hsub2(prmt(x, magic, 0x5150), 0x64806480u), sc[0]);
-          a[1] = hmul2(hsub2(prmt(x, magic, 0x5352), 0x64806480u), sc[0]);
-          a[2] = hmul2(hsub2(prmt(y, magic, 0x5150), 0x64806480u), sc[1]);
-          a[3] = hmul2(hsub2(prmt(y, magic, 0x5352), 0x64806480u), sc[1]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[r * 8 + 2 * w + h][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
+          const uint32_t w4[4] = {hsub2(prmt(x, magic, 0x5150), 0x64806480u), hsub2(prmt(x, magic, 0x5352), 0x64806480u),
+                                  hsub2(prmt(y, magic, 0x5150), 0x64806480u), hsub2(prmt(y, magic, 0x5352), 0x64806480u)};
+          value_product<NT, REST>(o[r * 8 + 2 * w + h], w4, sc, p);
         }
       } else {
 #pragma unroll
@@ -182,13 +196,10 @@ __device__ __forceinline__ void value_step(float (&o)[D / 16][NT][4], const uint
           uint32_t x = prmt(v[0][w], v[1][w], q ? 0x7632 : 0x5410), y = prmt(v[2][w], v[3][w], q ? 0x7632 : 0x5410);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t a[4];
-            a[0] = hmul2(hsub2(and_or<0x000F000Fu>(x, magic), 0x64086408u), sc[0]);
-            a[1] = hmul2(hfma2(and_or<0x00F000F0u>(x, magic), 0x2C002C00u, 0xD480D480u), sc[0]);
-            a[2] = hmul2(hsub2(and_or<0x000F000Fu>(y, magic), 0x64086408u), sc[1]);
-            a[3] = hmul2(hfma2(and_or<0x00F000F0u>(y, magic), 0x2C002C00u, 0xD480D480u), sc[1]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(o[4 * w + 2 * q + h][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
+            const uint32_t w4[4] = {
+                hsub2(and_or<0x000F000Fu>(x, magic), 0x64086408u), hfma2(and_or<0x00F000F0u>(x, magic), 0x2C002C00u, 0xD480D480u),
+                hsub2(and_or<0x000F000Fu>(y, magic), 0x64086408u), hfma2(and_or<0x00F000F0u>(y, magic), 0x2C002C00u, 0xD480D480u)};
+            value_product<NT, REST>(o[4 * w + 2 * q + h], w4, sc, p);
             x >>= 8, y >>= 8;
           }
         }
@@ -458,8 +469,8 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         mbar_wait(bars + out_slot * 8, phase, in_time);
         const uint32_t vb = ring + out_slot * P::kHalf;
         const int lim = see_max + 1 - key0;
-        value_step<D, BITS, NT>(o, p[0], vb, 0, lane, edge, lim, magic);
-        value_step<D, BITS, NT>(o, p[1], vb, 1, lane, edge, lim, magic);
+        value_step<D, BITS, NT, !BF16>(o, p[0], vb, 0, lane, edge, lim, magic);
+        value_step<D, BITS, NT, !BF16>(o, p[1], vb, 1, lane, edge, lim, magic);
         if (edge) {
           // value_step took non-finite scales for 0, so that rows that do not see such a key stay clean; the rows that do become NaN
           bool odd = false;

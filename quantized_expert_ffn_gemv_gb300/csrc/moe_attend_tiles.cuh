@@ -20,7 +20,7 @@
 // An fp16 K has 11 bits where integer times scale has up to 19.  That is
 // within what outputs of bf16 show; with fp16 activations it was the largest
 // error (5.4e-4 of the output, of 2.1e-4 for its own rounding), so there the
-// rest of K, exact in fp16 too, is a second operand of S.
+// rest of K, exact in fp16 too, is a second operand of S, and P's of O.
 // Registers move from the dequantising warps to the softmax (setmaxnreg).
 // The two row tiles share the dequantised keys and keep the tensor core busy
 // while the other's softmax runs.  A step of 64 keys (heads of 128, 256 rows)
@@ -53,7 +53,7 @@ struct TilesPlan {
   static constexpr int NRT = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * NRT;
   static constexpr int kHalf = kv_half_bytes(D, BITS);
-  static constexpr bool kRest = !BF16;                           // K's rest, too
+  static constexpr bool kRest = !BF16;                           // K's and P's rests, too
   static constexpr int kHalves = D == 256 && (BITS == 8 || kRest) ? 1 : 2;  // half tiles of a ring entry
   static constexpr int kEntry = kHalves * kHalf;
   static constexpr int kEntries = D == 256 ? (kRest ? (BITS == 8 ? 2 : 3) : 4) : 3;  // of either ring
@@ -502,8 +502,10 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
             mbar_wait(bar(kPFull + 2 * i + pb), (of >> 1) & 1, ok);
             tc_after();
             static_assert(kKeys == 64, "one call");
-            tc_mma4_ts<2048 / 16>(tmem + P::kTmemO + i * D, tmem + (2 * i + pb) * kKeys, desc_mn(sm + P::kOffV + st * P::kStage, kKeys * 128), kIdO,
-                                  j > 1);
+            const uint32_t from = tmem + (2 * i + pb) * kKeys, o = tmem + P::kTmemO + i * D;
+            const uint64_t vd = desc_mn(sm + P::kOffV + st * P::kStage, kKeys * 128);
+            tc_mma4_ts<2048 / 16>(o, from, vd, kIdO, j > 1);
+            if (P::kRest) tc_mma4_ts<2048 / 16>(o, from + kKeys / 2, vd, kIdO, 1);
             tc_commit(bar(kODone + i));
             tc_commit(bar(kVEmpty + st));
           }
@@ -662,15 +664,17 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t ph[16];
+          uint32_t ph[16], rest[16];
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
             const float e0 = ex2(fmaf(__uint_as_float(s[h][x]), c, z));
             const float e1 = ex2(fmaf(__uint_as_float(s[h][x + 1]), c, z));
             l4[(x >> 1) & 3] += e0 + e1;
             ph[x >> 1] = pack2<false>(e0, e1);
+            if (P::kRest) rest[x >> 1] = rest_of(ph[x >> 1], e0, e1);
           }
           tc_st16(t_s + h * 16, ph);
+          if constexpr (P::kRest) tc_st16(t_s + kKeys / 2 + h * 16, rest);
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         // the previous step's product is done by now; seeing each one keeps the barrier's phase known

@@ -34,7 +34,8 @@ def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False, keys_rounded=F
     sum of its products' magnitudes (fp32 accumulation of D / 16 steps, two scalings, the exponential), which moves a term by
     2 delta relative; then half a step of the output's type.  With more than 64 rows a sequence (16 of heads of 256), or behind a
     shared prefix, the keys, integer times scale, are rounded to fp16 too: delta grows by 2^-11 of the same sum; with fp16
-    activations by 2^-22, a rounding of what that left (and 2^-24 |q| where the rest is subnormal: keys here are not that small)."""
+    activations by 2^-22, a rounding of what that left (and 2^-24 |q| where the rest is subnormal: keys here are not that small),
+    and either the probabilities' or the values' rounding is taken up the same way."""
     import torch
     D, at = q.shape[2], 0
     group = q.shape[1] // kv[0][0].shape[1]
@@ -50,15 +51,15 @@ def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False, keys_rounded=F
         sums = np.einsum("nhd,lhd->nhl", np.abs(qs), np.abs(kg)).max(-1) * abs(scale) if length else np.zeros(qs.shape[:2])
         delta = ((D / 16 + 4) * 2.0 ** -21 + keys_rounded) * sums
         big = np.abs(vg).max(0)[None] if length else 0.0
-        tol = (2 * 2.0 ** -11 + 2.0 ** -18 + 2 * delta[..., None]) * mean_abs * 1.01 + max(length, 1) * 2.0 ** -32 * big
+        tol = ((2 if dt == torch.bfloat16 else 1) * 2.0 ** -11 + 2.0 ** -18 + 2 * delta[..., None]) * mean_abs * 1.01 + max(length, 1) * 2.0 ** -32 * big
         tol = tol + eps / 2 * (np.abs(want) + tol) + 2.0 ** -25
         err = np.abs(got - want)
         assert (err <= tol).all(), (float((err / tol).max()), n, length)
         if ordinary and length:
             # of the norm: roundings are independent, uniform within half a step (1 / sqrt 3 of it).  Keys move a score by 2^-11 /
-            # sqrt 3 of the root of its squared products' sum, which is the queries' size, 2; then P, V and the output
+            # sqrt 3 of the root of its squared products' sum, which is the queries' size, 2; then P and V (one of them with fp16) and the output
             step = 2.0 ** -11 / 3 ** 0.5
-            bound = ((2 * step) ** 2 * (keys_rounded > 2.0 ** -12) + 2 * step ** 2 + (eps / 2) ** 2 / 3) ** 0.5
+            bound = ((2 * step) ** 2 * (keys_rounded > 2.0 ** -12) + (2 if dt == torch.bfloat16 else 1) * step ** 2 + (eps / 2) ** 2 / 3) ** 0.5
             assert np.linalg.norm(err) <= 1.7 * bound * np.linalg.norm(want), np.linalg.norm(err) / np.linalg.norm(want)
         seen = np.isfinite(want_l)
         assert np.array_equal(seen, np.isfinite(got_l))
