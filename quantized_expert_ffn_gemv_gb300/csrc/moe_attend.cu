@@ -255,14 +255,16 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   st = device_sms(&sms);
   if (st != MOE_OK) return st;
   // A sequence's rows in tiles of 8 while they suffice, then 16 and 32, which
-  // share the dequantised keys and values.  Above 64 rows the tensor cores'
-  // tiles of 256 (128 for heads of 256); heads of 256, which have registers for
-  // 16 rows on the other path, above 16: 12 sequences of 60,000 to 131,072
-  // tokens at 32 rows take 265 us there and 328 in tiles of 16.  Heads of 128
-  // take 109 and 111 us at 32 rows (32 sequences of 8,192).
+  // share the dequantised keys and values.  Above one such tile (two of them
+  // for heads of 64) the tensor cores' tiles of 256, 128 for heads of 256.  In
+  // us there and here, 32 sequences of 8,192 tokens, 4 kv heads of 128, 8 bits:
+  // 32 rows 136 and 109, 48 rows 138 and 188, 64 rows 140 and 193 (4 bits 140
+  // and 107, 142 and 185, 145 and 190); heads of 64, 64 rows: 135 and 117 (4 bits
+  // 99 and 112).  Heads of 256, which have registers for 16 rows here: 12
+  // sequences of 60,000 to 131,072 tokens in 4 bits, 32 rows, 226 and 328.
   const int dim = cache->head_dim, heads = cache->n_kv_heads, group = n_q / heads;
   const int big = dim == 256 ? 128 : 256;
-  p->tiles = rows > (dim == 256 ? 16 : 64);
+  p->tiles = rows > (dim == 256 ? 16 : dim == 128 ? 32 : 64);
   p->tile_rows = p->tiles ? big : rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32;
   p->parts = p->tiles ? sms : sms * rows_blocks(dim, cache->bits, p->tile_rows);
   p->max_row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);

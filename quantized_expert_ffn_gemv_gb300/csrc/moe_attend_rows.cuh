@@ -12,8 +12,8 @@
 //
 // The products run on mma.sync m16n8k16 with keys (or output elements) as M
 // and rows as N, so that a group of 8 query heads fills the tile: with rows
-// as M half of it was padding, and the warp instructions a tile went from
-// 1,112 to about 600, which is what bounds the 4-bit case.  S^T = K Q^T has its
+// as M half of it was padding.  Warp instructions bound the 4-bit case: 64
+// sequences of 8,192 tokens take 80 us (45 of memory time), in 8 bits 103 (84).  S^T = K Q^T has its
 // probabilities transposed in registers (movmatrix) into the operand of
 // O^T = V^T P^T.
 //

@@ -32,7 +32,7 @@ def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False, keys_rounded=F
     """Per element.  A probability and a value are rounded to fp16 once each (2^-11 of the term; probabilities below
     fp16's normal range, which are held times 2^8, by 2^-33 of the largest), a score is off by delta <= (D / 16 + 4) 2^-21 of the
     sum of its products' magnitudes (fp32 accumulation of D / 16 steps, two scalings, the exponential), which moves a term by
-    2 delta relative; then half a step of the output's type.  With more than 64 rows a sequence (16 of heads of 256), or behind a
+    2 delta relative; then half a step of the output's type.  With more than 64 rows a sequence (32 of heads of 128, 16 of 256), or behind a
     shared prefix, the keys, integer times scale, are rounded to fp16 too: delta grows by 2^-11 of the same sum; with fp16
     activations by 2^-22, a rounding of what that left (and 2^-24 |q| where the rest is subnormal: keys here are not that small),
     and either the probabilities' or the values' rounding is taken up the same way."""
@@ -40,7 +40,7 @@ def check(q, out, lse, kv, news, lens, scale, dt, ordinary=False, keys_rounded=F
     D, at = q.shape[2], 0
     group = q.shape[1] // kv[0][0].shape[1]
     eps = torch.finfo(dt).eps
-    keys_rounded = (2.0 ** -11 if dt == torch.bfloat16 else 2.0 ** -22) if keys_rounded or max(news) * group > (16 if D == 256 else 64) else 0.0
+    keys_rounded = (2.0 ** -11 if dt == torch.bfloat16 else 2.0 ** -22) if keys_rounded or max(news) * group > {64: 64, 128: 32, 256: 16}[D] else 0.0
     for (k, v), n, length in zip(kv, news, lens):
         if n == 0:
             continue
