@@ -134,7 +134,7 @@ typedef struct {
   int32_t n_seqs;             /* 1..65536 */
   int32_t table_stride;       /* entries from one row of block_table to the next, >= max_pages */
   int32_t max_pages;          /* entries of a row, >= 1; max_pages * page_size < 2^31 */
-  int32_t n_tokens;           /* rows of q, k, v and the outputs, >= cu_tokens[n_seqs]; 0: the call does nothing */
+  int32_t n_tokens;           /* rows of q, k, v and the outputs, >= cu_tokens[n_seqs], < 2^31 - 256; 0: the call does nothing */
   int32_t max_tokens;         /* the most new tokens of one sequence, 1..n_tokens */
 } moe_kv_batch_t;
 

@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
 #pragma unroll
   for (int i = 0; i < NE; ++i) o[i] = 0.f;
   const int see = sq.len - sq.n + tok - sq.row0;
-  if (see >= 0) {
-    const int n = min(max(__ldg(a.cu + a.n_seqs), 0), a.n_tokens), tiles = (n * t.group + pre.tile_rows - 1) / pre.tile_rows;
+  const int n = min(max(__ldg(a.cu + a.n_seqs), 0), a.n_tokens);
+  if (see >= 0 && tok < n) {  // (a batch whose token counts decrease, which is flagged, has rows that the prefix's pass did not see)
+    const int tiles = (n * t.group + pre.tile_rows - 1) / pre.tile_rows;
     const int fr = tok * t.group + g, rt = fr / pre.tile_rows;
     merge_span<D>(pre, (int64_t)head * tiles + rt, fr - rt * pre.tile_rows, lane, m, l, o);
   }
@@ -249,7 +250,7 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   if (st != MOE_OK) return st;
   if (n_q < 1 || n_q % cache->n_kv_heads || shared_tokens < 0 || shared_tokens % cache->page_size) return MOE_ERR_INVALID_ARG;
   if (shared_tokens / cache->page_size > batch->max_pages) return MOE_ERR_INVALID_ARG;
-  const int64_t rows = (int64_t)batch->max_tokens * (n_q / cache->n_kv_heads);
+  const int64_t rows = batch->n_tokens ? (int64_t)batch->max_tokens * (n_q / cache->n_kv_heads) : 0;
   if (rows > 1 << 24) return MOE_ERR_UNSUPPORTED;
   int sms = 0;
   st = device_sms(&sms);

@@ -12,6 +12,8 @@
 
 namespace moe {
 
+constexpr int kMaxTokens = INT32_MAX - 256;  // a block's tokens more still fit an int
+
 moe_status_t kv_args(const moe_kv_cache_t* c, const moe_kv_batch_t* b, KvArgs* out) {
   if (!c || !b || !c->data || !c->status || !b->block_table || !b->seq_lens || !b->cu_tokens) return MOE_ERR_INVALID_ARG;
   if (((uintptr_t)c->data & 15) || ((uintptr_t)c->status & 3) || ((uintptr_t)b->block_table & 3) ||
@@ -19,7 +21,8 @@ moe_status_t kv_args(const moe_kv_cache_t* c, const moe_kv_batch_t* b, KvArgs* o
     return MOE_ERR_INVALID_ARG;
   const size_t page = moe_kv_page_bytes(c->page_size, c->n_kv_heads, c->head_dim, c->bits);
   if (!page || c->n_pages < 1 || c->data_bytes / page < (size_t)c->n_pages) return MOE_ERR_INVALID_ARG;
-  if (b->n_seqs < 1 || b->n_seqs > 65536 || b->max_pages < 1 || b->table_stride < b->max_pages || b->n_tokens < 0)
+  if (b->n_seqs < 1 || b->n_seqs > 65536 || b->max_pages < 1 || b->table_stride < b->max_pages || b->n_tokens < 0 ||
+      b->n_tokens > kMaxTokens)
     return MOE_ERR_INVALID_ARG;
   if ((int64_t)b->max_pages * c->page_size > INT32_MAX) return MOE_ERR_INVALID_ARG;
   if (b->n_tokens > 0 && (b->max_tokens < 1 || b->max_tokens > b->n_tokens)) return MOE_ERR_INVALID_ARG;
@@ -468,7 +471,7 @@ extern "C" MOE_API moe_status_t moe_qk_norm_rope(const moe_norm_rope_t* desc, in
                                                  const moe_heads_t* k_out, const int32_t* positions, void* cuda_stream) {
   moe_status_t st = moe::half_type(dtype);
   if (st != MOE_OK) return st;
-  if (n_tokens < 0 || head_dim < 8 || head_dim > 256 || head_dim % 8 || n_q < 0 || n_kv < 0 || n_q > 65536 || n_kv > 65536)
+  if (n_tokens < 0 || n_tokens > moe::kMaxTokens || head_dim < 8 || head_dim > 256 || head_dim % 8 || n_q < 0 || n_kv < 0 || n_q > 65536 || n_kv > 65536)
     return MOE_ERR_INVALID_ARG;
   moe::RowArgs r{};
   st = moe::norm_args(desc, head_dim, positions, n_tokens > 0, &r);

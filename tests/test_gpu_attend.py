@@ -250,6 +250,19 @@ def test_shared_prefix_captured_and_with_a_bad_page():
             assert bad[at:at + n].isnan().all() if length > 192 else torch.equal(bad[at:at + n], eager[at:at + n])
         at += n
 
+
+def test_shared_prefix_with_token_counts_that_decrease():
+    """The last sequence's rows would end before they begin: the batch is flagged, the sequences before it that end in time are right."""
+    from quantized_expert_ffn_gemv_gb300 import moe
+    share = 1024
+    cache, batch, _, q, _, news, lens = shared_case(8, 128, 4, 2, share, 280)
+    want = cache.attend(q, batch, shared_tokens=share)
+    batch._tensors[2][-1] = 40
+    got = cache.attend(q, batch, shared_tokens=share)
+    with pytest.raises(moe.MoeError, match="bad batch"):
+        cache.check()
+    assert (got[:40] - want[:40]).abs().max() <= 0.02 * want.abs().max()  # (cut into other parts: each within a bf16 step, 2^-8, and 2^-9)
+
 @pytest.mark.parametrize("n,group", [(1, 4), (3, 2), (100, 2)])
 def test_rows_that_see_nothing(n, group):
     """More new tokens than positions: the first rows see nothing, out 0 and lse -infinity; the batch is flagged."""

@@ -117,6 +117,7 @@ def test_norm_rope_refuses(moe):
     assert call(None) == INVALID and call(ok, pos=None) == INVALID and call(ok, pos=ADDR + 1) == INVALID
     assert call(ok, T=-1) == INVALID and call(ok, dim=100) == INVALID and call(ok, dim=264) == INVALID
     assert call(ok, nq=-1) == INVALID and call(ok, nk=-1) == INVALID
+    assert call(ok, T=2 ** 31 - 1) == INVALID
     assert call(ok, nq=65535) == UNSUPPORTED and call(ok, nq=1, nk=65535) == UNSUPPORTED
     assert call(ok, dtype=2) == UNSUPPORTED and call(ok, dtype=9) == INVALID
     for kw in BAD_HEADS:
