@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const KvArgs 
 // Merges a segment's parts, or its whole, into a row's running result; the warp's lanes hold D / 32 elements each.
 template <int D>
 __device__ __forceinline__ void merge_span(const AttArgs& t, int64_t segment, int row, int lane, float& m, float& l, float (&o)[D / 32]) {
-  constexpr int NE = D / 32, kAhead = 4;
+  constexpr int NE = D / 32, kAhead = D == 256 ? 4 : 8;
   const Span s = t.spans[segment];
   const bool whole = s.first == kWhole;
   const int c0 = whole ? 0 : s.first, c1 = whole ? 0 : s.last;
@@ -270,13 +270,14 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   p->parts = p->tiles ? sms : sms * rows_blocks(dim, cache->bits, p->tile_rows);
   p->max_row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
   // A prefix gets a pass of its own where that spares the rows' kernel a
-  // million keys (counted a kv head); the pass and the merge of its results
-  // take as long.  In us, with the pass and without (where all but the first
-  // read come from L2), 8 bits, heads of 128, 4 kv heads: 64 sequences x 2,048
-  // tokens (0.5 million) 42 and 33, 16 x 16,384 (1.0) 42 and 43, 64 x 4,096
-  // (1.0) 45 and 48, 128 x 4,096 (2.1) 53 and 85, 48 x 16,384 (3.1) 57 and 108.
-  // 4 bits, 64 x 4,096: 43 and 48; heads of 256, 2 kv heads, 16 x 16,384 (0.5)
-  // 61 and 41, 16 x 32,768 (1.0) 66 and 68; of 64, 8 kv heads, 64 x 4,096 (2.1) 40 and 58.
+  // million keys (counted a kv head), whose reading takes about as long as the
+  // pass and the merge.  In us, with the pass and without (where all but the
+  // first read come from L2), 8 bits, heads of 128, 4 kv heads: 16 sequences x
+  // 16,384 tokens (1.0 million) 37 and 42, 64 x 4,096 (1.0) 41 and 48, 128 x
+  // 4,096 (2.1) 53 and 84, 48 x 16,384 (3.1) 52 and 106; 64 x 2,048 (0.5) 33
+  // without, and with one that the rows' kernel had to wait for 42.  4 bits, 64
+  // x 4,096: 40 and 48; heads of 256, 2 kv heads, 16 x 32,768 (1.0) 63 and 68;
+  // of 64, 8 kv heads, 64 x 4,096 (2.1) 36 and 58.
   const int64_t all_rows = (int64_t)batch->n_tokens * group;
   const int64_t passes = std::max<int64_t>(all_rows / p->tile_rows, std::min(batch->n_seqs, batch->n_tokens));
   p->shared = !p->tiles && (double)(passes - 1) * shared_tokens * heads >= 0.98e6 ? shared_tokens : 0;

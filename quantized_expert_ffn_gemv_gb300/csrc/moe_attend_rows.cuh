@@ -271,7 +271,10 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
   }
   __syncthreads();
   grid_launch_dependents();
-  if (w0 >= total) return;
+  if (w0 >= total) {
+    if (t.shared) grid_wait();
+    return;
+  }
 
   int b = s_b;
   long long base = s_base, cur = w0;
@@ -577,6 +580,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
       }
     }
   }
+  if (t.shared) grid_wait();  // the merge waits for this kernel, and through it for the prefix's pass
 }
 
 template <int D, int BITS, bool BF16, int NT>
@@ -584,8 +588,22 @@ moe_status_t launch_rows_kernel(const KvArgs& kv, const AttArgs& t, cudaStream_t
   constexpr int smem = RowsPlan<D, BITS, NT>::kSmem;
   const moe_status_t ok = raise_smem<attend_rows_kernel<D, BITS, BF16, NT>>(smem);
   if (ok != MOE_OK) return ok;
-  attend_rows_kernel<D, BITS, BF16, NT><<<t.parts, kAttThreads, smem, st>>>(kv, t);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (!t.shared) {
+    attend_rows_kernel<D, BITS, BF16, NT><<<t.parts, kAttThreads, smem, st>>>(kv, t);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  // beside the prefix's pass, which it does not read, as SMs become free
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)t.parts);
+  cfg.blockDim = dim3(kAttThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_rows_kernel<D, BITS, BF16, NT>, kv, t) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 template <int D, int BITS, bool BF16>

@@ -26,6 +26,7 @@
 // tried first: the k-th largest of those is at most the k-th of all, and
 // seldom many lie between.
 #include <cooperative_groups.h>
+#include <algorithm>
 #include <cmath>
 
 #include "moe_kv.cuh"
@@ -69,6 +70,7 @@ struct SampleArgs {
   const void* logits;
   int64_t row_stride;
   int rows, vocab, slice;
+  int ahead;  // rows that run at a time
   const float *u, *temperature, *top_p, *min_p;
   const int32_t* top_k;
   int32_t* tokens;
@@ -764,6 +766,12 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     }
   }
   for (int i = head + vecs * kVec + tid; i < n; i += kSThreads) put(i, as_f32(src[i]));
+  // the slice that is read when this one's place is free, into L2 while the row is worked on
+  if (tid == 0 && row < a.rows - a.ahead) {
+    const uintptr_t from = (uintptr_t)(src + (int64_t)a.ahead * a.row_stride), at = (from + 15) & ~(uintptr_t)15;
+    const uintptr_t bytes = (from + (uintptr_t)n * sizeof(T) - at) & ~(uintptr_t)15;
+    if (n * (int)sizeof(T) >= 32) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"((uint32_t)bytes) : "memory");
+  }
   const int n4 = (n + 3) / 4;
   if (tid < 4 * n4 - n) z[n + tid] = -INFINITY;
   for (int i = tid; i < kTable; i += kSThreads) s.pow2[i] = g_pow2.v[i];
@@ -929,6 +937,7 @@ moe_status_t launch_sample(SampleArgs a, cudaStream_t st) {
   const int smem = (int)sizeof(Shared) + a.slice * 4;
   ok = raise_smem<sample_kernel<T>>((int)sizeof(Shared) + kMaxVocab / kMaxCluster * 4);
   if (ok != MOE_OK) return ok;
+  a.ahead = std::max(1, sms * (smem <= 110 * 1024 ? 2 : 1) / C);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.rows * C));
   cfg.blockDim = dim3(kSThreads);
@@ -959,7 +968,7 @@ extern "C" MOE_API moe_status_t moe_sample(const void* logits, int32_t dtype, in
       ((uintptr_t)probs & 3))
     return MOE_ERR_INVALID_ARG;
   if (vocab > moe::kMaxVocab || rows > 1 << 28) return MOE_ERR_UNSUPPORTED;
-  const moe::SampleArgs a{logits, row_stride, rows, vocab, 0, u, temperature, top_p, min_p, top_k, tokens, probs};
+  const moe::SampleArgs a{logits, row_stride, rows, vocab, 0, 0, u, temperature, top_p, min_p, top_k, tokens, probs};
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   if (dtype == MOE_FP32) return moe::launch_sample<float>(a, s);
   if (dtype == MOE_BF16) return moe::launch_sample<__nv_bfloat16>(a, s);
