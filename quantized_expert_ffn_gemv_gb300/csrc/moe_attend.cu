@@ -259,9 +259,10 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   // share the dequantised keys and values.  Above one such tile (two of them
   // for heads of 64) the tensor cores' tiles of 256, 128 for heads of 256.  In
   // us there and here, 32 sequences of 8,192 tokens, 4 kv heads of 128, 8 bits:
-  // 32 rows 136 and 109, 48 rows 138 and 188, 64 rows 140 and 193 (4 bits 140
-  // and 107, 142 and 185, 145 and 190); heads of 64, 64 rows: 135 and 117 (4 bits
-  // 99 and 112).  Heads of 256, which have registers for 16 rows here: 12
+  // 32 rows 118 and 109, 48 rows 122 and 188, 64 rows 125 and 193 (4 bits 118
+  // and 107, 121 and 185, 124 and 190); heads of 64, 64 rows: 109 and 117 (4 bits
+  // 101 and 112; with fp16 activations the tiles take a third longer, rows do
+  // not).  Heads of 256, which have registers for 16 rows here: 12
   // sequences of 60,000 to 131,072 tokens in 4 bits, 32 rows, 226 and 328.
   const int dim = cache->head_dim, heads = cache->n_kv_heads, group = n_q / heads;
   const int big = dim == 256 ? 128 : 256;

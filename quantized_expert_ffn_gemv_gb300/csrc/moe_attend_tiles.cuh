@@ -26,8 +26,8 @@
 // while the other's softmax runs.  A step of 64 keys (heads of 128, 256 rows)
 // is 24 products, 1,240 cycles of the tensor core; one warp that issued both
 // tiles' products, with its waits and elections, took 2,500.  2,048 new tokens
-// of 4,096 (32 query and 4 kv heads of 128, 8 bits, bf16) take 242 us, 8,192 of
-// 16,384 1,395 (1,180 TFLOP/s); the chain of a step's softmax bounds them.
+// of 4,096 (32 query and 4 kv heads of 128, 8 bits, bf16) take 230 us, 8,192 of
+// 16,384 1,350 (1,220 TFLOP/s); the chain of a step's softmax bounds them.
 //
 // The line of work is measured in keys, causal limits included, so that all
 // parts cost the same: row tile rt of a sequence costs kSegmentKeys + the keys
@@ -46,7 +46,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kKeys = 64;           // keys of a step
-constexpr int kSegmentKeys = 512;   // what a segment costs beside its keys, in keys
+constexpr int kSegmentKeys = 768;   // what a segment costs beside its keys, in keys
 constexpr float kGrow = 7.f;        // log2 by which a maximum may outgrow its reference
 constexpr int kDeqWarps = 4;        // of either stream
 
@@ -170,6 +170,15 @@ struct Piece {
   Seq sq;
 };
 
+// a / b of numbers >= 0, mostly of 31 bits, when a shorter division does: 2,048
+// new tokens of 4,096 take 230 us with it and 242 without.  Not with row tiles
+// of 128 (heads of 256), where the rest of the kernel comes out slower for it:
+// 12 long sequences in 4 bits 226 us without and 245 with it.
+template <int ROWS>
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ROWS == 256 && ((a | b) >> 31) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The CTA's share of the line of work.  With a shared prefix there is one
 // sequence, `pre`: the new tokens of all, in front of them as many keys as the
 // prefix has (its len), read through the block table's row b.
@@ -196,7 +205,7 @@ struct Walk {
         ++b;
         continue;
       }
-      const int head = (int)(local / per_head);
+      const int head = (int)quotient<ROWS>(local, per_head);
       const long long x = local - head * per_head;
       int lo = 0, hi = n_rt - 1;
       while (lo < hi) {
@@ -215,7 +224,7 @@ struct Walk {
       const int lim = t.shared ? p.lim : min(s.len - s.n + last / t.group + 1, p.lim);
       p.steps = max(1, (lim + kKeys - 1) / kKeys);
       auto step_at = [&](long long pos) {
-        const long long u = pos / t.group - kSegmentKeys;
+        const long long u = quotient<ROWS>(pos, t.group) - kSegmentKeys;
         return (int)min((long long)p.steps, (max(u, 0ll) + kKeys - 1) / kKeys);
       };
       p.t0 = step_at(x0);
@@ -226,7 +235,7 @@ struct Walk {
       p.rt = lo;
       p.rows = s.n * t.group - lo * ROWS;
       p.sq = s;
-      p.first_part = (int)((seg_start + min((long long)t.group * (kSegmentKeys + 1), all) - 1) / part);
+      p.first_part = (int)quotient<ROWS>(seg_start + min((long long)t.group * (kSegmentKeys + 1), all) - 1, part);
       return true;
     }
     return false;
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
     walk.pre = Seq{0, n, min(t.shared, s_long[0]), false};
     total = n > 0 && walk.pre.len > 0 ? W::cost(t, walk.pre, W::row_tiles(t, walk.pre)) * a.heads : 0;
   }
-  walk.part = max((total + gridDim.x - 1) / gridDim.x, (long long)t.group * 2 * kKeys);
+  walk.part = max(quotient<P::kRows>(total + gridDim.x - 1, gridDim.x), (long long)t.group * 2 * kKeys);
   walk.cur = (long long)blockIdx.x * walk.part;
   walk.w1 = min(walk.cur + walk.part, total);
   if (t.shared) {
