@@ -66,8 +66,9 @@ struct TilesPlan {
   static constexpr int kOffV = kOffK + 2 * kKStage;
   static constexpr int kOffRaw = kOffV + 2 * kStage;
   static constexpr int kOffBar = (kOffRaw + 2 * kEntries * kEntry + 15) & ~15;
-  // barriers: raw full and empty of either ring, K full and empty, V full and empty, Q full, S full, P full, O done
-  static constexpr int kBars = 4 * kEntries + 8 + NRT * 6;
+  // barriers: raw full and empty of either ring, K full and empty, V full and empty, Q full, S full, P full, O done, pieces done
+  static constexpr int kSlots = 8;  // pieces under way at most
+  static constexpr int kBars = 4 * kEntries + 8 + NRT * 6 + kSlots;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSoftWarps = 4 * NRT;
   static constexpr int kThreads = 32 * (kSoftWarps + 2 * kDeqWarps + 4);
@@ -335,9 +336,11 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
   constexpr int kRawFull = 0, kRawEmpty = 2 * P::kEntries, kKFull = 4 * P::kEntries,  // raw: K's ring, then V's
                 kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
                 kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kSFull = kQFull + NRT, kPFull = kSFull + 2 * NRT,
-                kODone = kPFull + 2 * NRT;
+                kODone = kPFull + 2 * NRT, kPieceDone = kODone + NRT;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + P::kOffMisc);
-  int* s_bad = reinterpret_cast<int*>(smem + P::kOffMisc + 16);  // [8], by piece: position of the first bad page or non-finite V
+  // by piece: position of the first bad page or non-finite V.  The loader clears a slot before it loads the piece, when all
+  // softmax warps are done with the slot's last one (kPieceDone)
+  int* s_bad = reinterpret_cast<int*>(smem + P::kOffMisc + 16);
   int& s_b = *reinterpret_cast<int*>(smem + P::kOffMisc + 48);
   int* s_long = reinterpret_cast<int*>(smem + P::kOffMisc + 52);  // [2]
   long long& s_base = *reinterpret_cast<long long*>(smem + P::kOffMisc + 64);
@@ -364,9 +367,12 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
       }
       mbar_init(bar(kODone + i), 1);
     }
+    for (int i = 0; i < P::kSlots; ++i) mbar_init(bar(kPieceDone + i), P::kSoftWarps);
     fence_mbar_init();
   }
-  if (tid < 8) s_bad[tid] = INT32_MAX;
+  auto bad_of = [&](int piece) { return &s_bad[piece % P::kSlots]; };
+  // the slot's last piece has been finished by all
+  auto slot_wait = [&](int piece, bool& ok) { mbar_wait(bar(kPieceDone + piece % P::kSlots), ((piece / P::kSlots) & 1) ^ 1, ok); };
   constexpr int kIssueWarp = P::kSoftWarps + 2 * kDeqWarps, kLoadWarp = kIssueWarp + 1;  // (the second row tile's products: kIssueWarp + 2)
   if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "n"(P::kTmemCols));
@@ -440,6 +446,9 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
       int entry = 0, piece = 0;
       uint32_t phase = 1;  // the ring starts empty
       for (; walk.next(a, t, p); ++piece) {
+        slot_wait(piece, ok);
+        if (lane == 0) *bad_of(piece) = INT32_MAX;
+        __syncwarp();
         const int lim = p.lim;
         const int n32 = 2 * (p.t1 - p.t0);
         const uint8_t* src = nullptr;
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
               pi = kv_page_of(a, pos);
               page = __ldg(a.table + (size_t)p.b * a.table_stride + pi);
               if ((unsigned)page >= (unsigned)a.n_pages) {
-                atomicMin(&s_bad[piece & 7], pos);
+                atomicMin(bad_of(piece), pos);
                 kv_flag(a, MOE_KV_BAD_PAGE);
                 page = 0;  // in bounds; the rows that see it become NaN
               }
@@ -535,7 +544,6 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
     int entry = 0;
     uint32_t phase = 0, step = 0;
     for (int piece = 0; walk.next(a, t, p); ++piece) {
-      if (v && dt == 0) s_bad[(piece + 4) & 7] = INT32_MAX;  // (no warp is more than three pieces from another)
       const int lim = p.lim;
       for (int j = p.t0; j < p.t1; ++j, ++step) {
         const uint32_t st = step & 1;
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
           mbar_wait(bar(kRawFull + e), phase, ok);
           dequantise<D, BITS, P::kHalves, P::kRest>(sm + P::kOffRaw + e * P::kEntry,
                                                     sm + (v ? P::kOffV + st * P::kStage : P::kOffK + st * P::kKStage), h * kKvTile, dt, v,
-                                                    lim - pos0, pos0, &s_bad[piece & 7], magic);
+                                                    lim - pos0, pos0, bad_of(piece), magic);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kRawEmpty + e));
           if (++entry == P::kEntries) entry = 0, phase ^= 1;
@@ -564,7 +572,14 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
     const uint32_t t_o = tmem + P::kTmemO + i * D + lanes;
     uint32_t step = 0;
     for (int piece = 0; walk.next(a, t, p); ++piece) {
-      if (i * 128 >= p.rows) continue;  // no rows in this tile
+      auto finished = [&]() {
+        if (lane == 0) mbar_arrive(bar(kPieceDone + piece % P::kSlots));
+      };
+      if (i * 128 >= p.rows) {  // no rows in this tile
+        slot_wait(piece, ok);   // (nothing else holds the warp back)
+        finished();
+        continue;
+      }
       const int fr = p.rt * P::kRows + i * 128 + row, tok = fr / t.group, gh = fr - tok * t.group;
       bool live = fr < p.sq.n * t.group;
       int see = live ? p.sq.len - p.sq.n + tok : -1;  // the last position that the row sees
@@ -630,6 +645,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
           if (lane == 0) mbar_arrive(bar(kPFull + 2 * i + (step & 1)));
         }
         mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
+        finished();
         continue;
       }
       const int see_all = __reduce_min_sync(0xffffffffu, live ? see : INT32_MAX);  // up to here no key is hidden from a row of the warp
@@ -697,7 +713,9 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
       }
       mbar_wait(bar(kODone + i), (step - 1) & 1, ok);
       tc_after();
-      const int bad = *(volatile int*)&s_bad[piece & 7];
+      const int bad = *(volatile int*)bad_of(piece);
+      __syncwarp();
+      finished();
       if (bad <= see || (p.sq.over && see >= a.max_pages * a.page_size)) l = __uint_as_float(kNaN);
       if (!ok) {
         if (lane == 0) kv_flag(a, MOE_KV_TIMEOUT);
