@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
     const int nt = (t1 - t0 - warp + kAttWarps - 1) / kAttWarps;
     int first = 0;
     const uint8_t* mine_src = nullptr;
-    bool bad_page = false;
+    int bad = INT32_MAX;  // the first position on a bad page that the lane looked up
     auto load_pages = [&](int from) {
       first = from;
       const int i = from + lane;
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         const int pos = t.shared + (t0 + warp + kAttWarps * i) * kKvTile, pi = kv_page_of(a, pos);
         int page = pi < a.max_pages ? __ldg(a.table + (size_t)b * a.table_stride + pi) : -1;
         if ((unsigned)page >= (unsigned)a.n_pages) {
-          if (sq.len > 0) bad_page = true;  // an empty sequence's one tile holds nothing that is seen
-          page = 0;                         // in bounds; the rows become NaN
+          if (sq.len > 0) bad = min(bad, pos);  // an empty sequence's one tile holds nothing that is seen
+          page = 0;                             // in bounds; the rows that see it become NaN
         }
         mine_src = a.data + (size_t)page * a.page_bytes + (size_t)head * a.head_bytes +
                    (size_t)((pos - pi * a.page_size) / kKvTile) * (2 * P::kHalf);
@@ -492,14 +492,12 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         release();
       }
     }
-    bool spoiled = false;
-    if (__any_sync(0xffffffffu, bad_page) || sq.over) {
-      if (lane == 0) kv_flag(a, MOE_KV_BAD_PAGE);
-      spoiled = true;
-    }
+    bad = __reduce_min_sync(0xffffffffu, bad);
+    if (bad != INT32_MAX && lane == 0) kv_flag(a, MOE_KV_BAD_PAGE);
+    if (sq.over) bad = min(bad, a.max_pages * a.page_size);  // (flagged with the batch)
     if (!in_time) {
       if (lane == 0) kv_flag(a, MOE_KV_TIMEOUT);
-      spoiled = true;
+      bad = INT32_MIN;
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -507,7 +505,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int of = 4; of < 32; of <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], of);
-        if (spoiled) l[n][h] = __uint_as_float(kNaN);
+        if (see[n][h] >= bad) l[n][h] = __uint_as_float(kNaN);
         if (g == 0) s_stat[warp][8 * n + 2 * tq + h] = make_float2(m[n][h], l[n][h]);
       }
 

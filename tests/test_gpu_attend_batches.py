@@ -63,3 +63,40 @@ def test_bad_pages_among_many_short_prompts(bits, dim, dtype):
         rows = got.flatten(1).cpu()
         assert rows[spoiled].isnan().all()
         assert torch.equal(rows[~spoiled], clean.flatten(1).cpu()[~spoiled])
+
+
+@pytest.mark.parametrize("n,dim,bits", [(4, 128, 8), (6, 64, 4), (5, 256, 4), (70, 128, 8), (70, 256, 4)])
+def test_a_bad_page_reaches_only_the_rows_that_see_it(n, dim, bits):
+    """New tokens on both sides of a page's end: with the second page out of range, or behind the table's width, the rows
+    before it keep their bits."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import attention, moe
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()
+    page, first = 32, n // 2
+    start = 3 * page - first  # position of the first new token: `first` of them lie on the third page
+    lens = [start + n, start + n + 5]
+    rng = np.random.default_rng(n)
+    batch, table, n_pages = make_batch([n, n], lens, page, rng)
+    cache = attention.KvCache(n_pages, page, 2, dim, bits)
+    cache.data.fill_(0xFF)
+    fill(cache, table, lens)
+    q = torch.randn(2 * n, 4, dim).bfloat16().cuda()
+    clean = cache.attend(q, batch)
+    cache.check()
+    assert clean.isfinite().all()
+    bad = table.copy()
+    bad[0, 3] = -7
+    wide = attention.KvBatch(i32(*bad.tolist()), i32(*lens), i32(0, n, 2 * n), 2 * n, n)
+    got = cache.attend(q, wide)
+    with pytest.raises(moe.MoeError, match="bad page"):
+        cache.check()
+    assert torch.equal(got[:first], clean[:first]) and got[first:n].isnan().all() and torch.equal(got[n:], clean[n:])
+    narrow = attention.KvBatch(wide._tensors[0][:, :3], i32(*lens), i32(0, n, 2 * n), 2 * n, n)
+    got = cache.attend(q, narrow)
+    with pytest.raises(moe.MoeError, match="bad page"):
+        cache.check()
+    for at, seen in ((0, first), (n, max(0, first - 5))):
+        rows = got[at:at + n]
+        assert rows[seen:].isnan().all()
+        # (cut into other parts when shorter: each result within a bf16 step, 2^-8, of the same number)
+        assert (rows[:seen].float() - clean[at:at + seen].float()).abs().max() <= 2.0 ** -7 * clean.abs().max() if seen else True
