@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
     const int fr = (tok - sq.row0) * t.group + g, rt = fr / t.tile_rows;
     merge_span<D>(t, ((int64_t)b * a.heads + head) * t.max_row_tiles + rt, fr - rt * t.tile_rows, lane, m, l, o);
   }
+  if (see >= a.max_pages * a.page_size) l = __uint_as_float(kNaN);  // (neither pass has a tile there where the prefix fills the table)
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* dst = t.out + (int64_t)tok * t.o_ts + (int64_t)qh * t.o_hs;
 #pragma unroll

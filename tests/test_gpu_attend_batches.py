@@ -2,8 +2,9 @@
 import numpy as np
 import pytest
 
-from tests.model_gpu import make_batch
-from tests.test_gpu_attend import fill, run_case
+from tests import model_ref as ref
+from tests.model_gpu import f64, make_batch, whole
+from tests.test_gpu_attend import check, fill, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -79,7 +80,7 @@ def test_a_bad_page_reaches_only_the_rows_that_see_it(n, dim, bits):
     batch, table, n_pages = make_batch([n, n], lens, page, rng)
     cache = attention.KvCache(n_pages, page, 2, dim, bits)
     cache.data.fill_(0xFF)
-    fill(cache, table, lens)
+    kv = fill(cache, table, lens)
     q = torch.randn(2 * n, 4, dim).bfloat16().cuda()
     clean = cache.attend(q, batch)
     cache.check()
@@ -92,11 +93,74 @@ def test_a_bad_page_reaches_only_the_rows_that_see_it(n, dim, bits):
         cache.check()
     assert torch.equal(got[:first], clean[:first]) and got[first:n].isnan().all() and torch.equal(got[n:], clean[n:])
     narrow = attention.KvBatch(wide._tensors[0][:, :3], i32(*lens), i32(0, n, 2 * n), 2 * n, n)
-    got = cache.attend(q, narrow)
+    lse = torch.zeros(2 * n, 4, device="cuda")
+    got = cache.attend(q, narrow, lse=lse)
     with pytest.raises(moe.MoeError, match="bad page"):
         cache.check()
-    for at, seen in ((0, first), (n, max(0, first - 5))):
-        rows = got[at:at + n]
-        assert rows[seen:].isnan().all()
-        # (cut into other parts when shorter: each result within a bf16 step, 2^-8, of the same number)
-        assert (rows[:seen].float() - clean[at:at + seen].float()).abs().max() <= 2.0 ** -7 * clean.abs().max() if seen else True
+    for b, seen in ((0, first), (1, max(0, first - 5))):
+        at = b * n
+        assert got[at + seen:at + n].isnan().all() and lse[at + seen:at + n].isnan().all()
+        check(f64(q)[at:at + seen], f64(got)[at:at + seen], f64(lse)[at:at + seen], [tuple(x[:3 * page] for x in kv[b])], [seen], [3 * page],
+              dim ** -0.5, torch.bfloat16, keys_rounded=n == 70)
+
+
+def prefix_case(bits, dim, dtype, page, share, seqs, group, hkv=4, tail=70, seed=0):
+    """Sequences behind a common prefix, of 1 to 3 new tokens or none, some that end inside it; share is a multiple of the page.
+    Returns (cache, batch, table, q, kv, news, lens), kv as held."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import attention
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    rng = np.random.default_rng(seed)
+    lens = [share + int(x) for x in rng.integers(0, tail, seqs)]
+    news = [1 + (i % 5 == 2) * 2 for i in range(seqs)]
+    lens[2:7], news[2:7] = [share, 1, share - 17, 0, share + 1], [3, 1, 2, 0, 1]
+    news[11] = 0
+    batch, table, n_pages = make_batch(news, lens, page, rng, share=share // page, wide=1)
+    cache = attention.KvCache(n_pages, page, hkv, dim, bits)
+    cache.data.fill_(0xFF)
+    base = torch.randn(2, share, hkv, dim, device="cuda").to(dt)
+    cache.append(base[0], base[1], whole(table[:1], [share]))
+    tails = [max(0, x - share) for x in lens]
+    own = torch.randn(2, sum(tails), hkv, dim, device="cuda").to(dt)
+    cu = np.concatenate(([0], np.cumsum(tails)))
+    dev = lambda a: torch.tensor(np.asarray(a).tolist(), dtype=torch.int32, device="cuda")
+    cache.append(own[0], own[1], attention.KvBatch(dev(table), dev(lens), dev(cu), int(cu[-1]), max(tails)))
+    cache.check()
+    hb, ho = [ref.held(f64(x), bits) for x in base], [ref.held(f64(x), bits) for x in own]
+    kv = [tuple(np.concatenate((hb[j][:min(share, x)], ho[j][cu[i]:cu[i + 1]])) for j in (0, 1)) for i, x in enumerate(lens)]
+    q = (torch.randn(batch.n_tokens, hkv * group, dim, device="cuda") * 2).to(dt)
+    assert (seqs - 30) * share * hkv > 1e6  # enough reads spared for a pass of its own
+    return cache, batch, table, q, kv, news, lens
+
+
+def test_a_length_beyond_the_table_behind_a_prefix_that_fills_it():
+    """The rows that lie behind the table's last page are NaN, as they are without the hint; the others keep their values."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import attention, moe
+    share, seqs, page = 1024, 300, 64
+    cache, _, table, _, kv, _, _ = prefix_case(8, 128, "bf16", page, share, seqs, 2)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    lens = [share] * seqs
+    lens[5], lens[17], lens[40] = share + 1, share + 40, share + 2  # one new token each, the last two of the fortieth
+    news = [1] * seqs
+    news[40] = 4
+    cu = np.concatenate(([0], np.cumsum(news))).tolist()
+    batch = attention.KvBatch(i32(table[:1, :share // page].repeat(seqs, 0).tolist()), i32(lens), i32(cu), cu[-1], 4)
+    q = (torch.randn(cu[-1], 8, 128, device="cuda") * 2).bfloat16()
+    outs = []
+    for shared in (0, share):
+        lse = torch.zeros(q.shape[:2], device="cuda")
+        outs.append((cache.attend(q, batch, lse=lse, shared_tokens=shared), lse))
+        with pytest.raises(moe.MoeError, match="bad page"):
+            cache.check()
+    beyond = torch.zeros(cu[-1], dtype=torch.bool)
+    beyond[[cu[5], cu[17], cu[40] + 2, cu[40] + 3]] = True
+    for out, lse in outs:
+        assert out.cpu()[beyond].isnan().all() and lse.cpu()[beyond].isnan().all()
+        assert out.cpu()[~beyond].isfinite().all()
+    # the sequences that fit the table, against binary64
+    fit = [i for i in range(seqs) if lens[i] == share]
+    rows = np.concatenate([np.arange(cu[i], cu[i + 1]) for i in fit])
+    for (out, lse), rounded in zip(outs, (False, True)):
+        check(f64(q)[rows], f64(out)[rows], f64(lse)[rows], [kv[2]] * len(fit), [1] * len(fit), [share] * len(fit), 128 ** -0.5,
+              torch.bfloat16, keys_rounded=rounded)
