@@ -164,3 +164,16 @@ def test_a_length_beyond_the_table_behind_a_prefix_that_fills_it():
     for (out, lse), rounded in zip(outs, (False, True)):
         check(f64(q)[rows], f64(out)[rows], f64(lse)[rows], [kv[2]] * len(fit), [1] * len(fit), [share] * len(fit), 128 ** -0.5,
               torch.bfloat16, keys_rounded=rounded)
+
+
+@pytest.mark.parametrize("bits,dim,dtype,page,share,seqs,group", [
+    (8, 128, "fp16", 64, 1024, 300, 2), (4, 256, "fp16", 32, 992, 320, 2), (8, 256, "fp16", 32, 1056, 300, 1), (4, 64, "fp16", 96, 1056, 290, 3),
+    (8, 64, "bf16", 32, 992, 300, 5), (4, 128, "bf16", 32, 1056, 300, 4), (8, 128, "bf16", 96, 1056, 300, 1), (4, 256, "bf16", 32, 1056, 290, 2)])
+def test_prefix_pass_of_either_type_and_page(bits, dim, dtype, page, share, seqs, group):
+    """A prefix that ends inside a step of 64 keys among them; both types."""
+    import torch
+    cache, batch, _, q, kv, news, lens = prefix_case(bits, dim, dtype, page, share, seqs, group)
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    out = cache.attend(q, batch, lse=lse, shared_tokens=share)
+    cache.check()
+    check(f64(q), f64(out), f64(lse), kv, news, lens, dim ** -0.5, q.dtype, keys_rounded=True)
