@@ -217,6 +217,7 @@ class KvCache:
         self.dev = _on_gpu(data, "data")
         self.data = data
         self._status = torch.zeros(1, dtype=_i32, device=data.device)
+        self._settle()  # calls on any stream come behind the zeros
         self.desc = moe.KvCacheDesc(data.data_ptr(), data.numel(), n_pages, page_size, n_kv_heads, head_dim, bits,
                                     self._status.data_ptr())
         self._at = C.addressof(self.desc)
@@ -347,11 +348,21 @@ class KvCache:
             moe.check(status, "moe_kv_attend")
         return out
 
+    def _settle(self):
+        """Wait for the current stream of the cache's device (a capture runs later, in its own order)."""
+        stream = torch.cuda.current_stream(self.dev)
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                stream.synchronize()
+
     def check(self):
-        """Synchronise, and raise MoeError if a call found a bad page, a bad
-        batch or ran out of a wait since the last check (which clears it)."""
+        """Wait for the device (all its streams), and raise MoeError if a call
+        found a bad page, a bad batch or ran out of a wait since the last
+        check (which clears it)."""
+        torch.cuda.synchronize(self.dev)
         bits = int(self._status.item())
         if bits:
             self._status.zero_()
+            self._settle()  # what later calls set on other streams is not cleared
             what = [n for b, n in ((BAD_PAGE, "bad page"), (BAD_BATCH, "bad batch"), (TIMEOUT, "timeout")) if bits & b]
             raise moe.MoeError(6 if bits & TIMEOUT else 8, "cache: " + ", ".join(what))
