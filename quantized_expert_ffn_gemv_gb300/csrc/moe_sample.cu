@@ -15,9 +15,9 @@
 // one that a first version used took half of its time.
 //
 // The cut.  Kept elements are a prefix of the order (logit descending, index
-// ascending).  A histogram of y (1/16 octave a bin; counts, and masses as two
-// 16-bit halves relative to the bin's octave) finds the bin the cut falls
-// into.  Each CTA lists its elements of that bin and those in front of it.
+// ascending).  A histogram of y (1/16 octave a bin; counts, or masses as two
+// 16-bit halves in units of which every weight of the bin is a whole number)
+// finds the bin the cut falls into.  Each CTA lists its elements of that bin and those in front of it.
 // If both fit one list, the first CTA ranks them all and draws the token by
 // itself; if only the bin's do, it ranks those for the cut's last element
 // and the cluster draws; otherwise the bin is histogrammed again, a thousand
@@ -117,15 +117,21 @@ __device__ __forceinline__ uint32_t weight31(float z, float m, const Rate& c, co
   s = (k >> 9) + 1;
   return (((__float_as_uint(t.x) & 0x7FFFFFu) | 0x800000u) << 7) + (uint32_t)(__float_as_int(low) - kMagicBits);
 }
-// W 2^(15 - s) rounded to units of 2^-45, with 32-bit shifts and one wide multiply.
-__device__ __forceinline__ uint64_t to_units(uint32_t W, int s) {
-  constexpr int kUp = kUnit - 30;
-  const uint32_t down = (uint32_t)max(s - kUp, 0);
-  const uint32_t mul = 1u << max(kUp - s, 0);
-  uint32_t half, w;
+// W 2^(15 - s) rounded to units of 2^-45 is v 2^up, with 32-bit shifts.
+constexpr int kUp = kUnit - 30;
+__device__ __forceinline__ uint32_t rounded(uint32_t W, int s) {
+  const uint32_t down = (uint32_t)(s - min(s, kUp));
+  uint32_t half, v;
   asm("shl.b32 %0, 1, %1;" : "=r"(half) : "r"(down));  // 0 from 32 on
-  asm("shr.u32 %0, %1, %2;" : "=r"(w) : "r"(W + (half >> 1)), "r"(down));
-  return (uint64_t)w * mul;
+  asm("shr.u32 %0, %1, %2;" : "=r"(v) : "r"(W + (half >> 1)), "r"(down));
+  return v;
+}
+__device__ __forceinline__ uint64_t to_units(uint32_t W, int s) { return (uint64_t)rounded(W, s) * (1u << (kUp - min(s, kUp))); }
+// The units that the masses of an octave's bins are held in: their weights have s = octave or octave + 1, so that each is a
+// whole number of 2^bin_unit, at most 2^31 1.022 of them.
+__device__ __forceinline__ int bin_unit(int octave) { return kUp - min(octave + 1, kUp); }
+__device__ __forceinline__ uint32_t in_bin_units(uint32_t W, int s, int octave) {
+  return rounded(W, s) << (min(octave + 1, kUp) - min(s, kUp));
 }
 __device__ __forceinline__ uint64_t weight(float z, float m, const Rate& c, const float2* tab) {
   int s;
@@ -468,7 +474,7 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         if (bin == kBins - 1) return;
         int sh;
         uint32_t W = weight31(z, v.m, v.c, s.pow2, sh);
-        W >>= sh - (level == 0 ? bin / kPerOctave : octave);  // relative to the bin's octave, which a weight is at most one below
+        W = in_bin_units(W, sh, level == 0 ? (int)((uint32_t)bin / kPerOctave) : octave);
         atomicAdd(&s.h.hi[bin], W >> 16);
         atomicAdd(&s.h.lo[bin], W & 0xFFFFu);
       } else if (bin == kBins - 1) {
@@ -491,9 +497,10 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         cnt += o->h.count[i];
         if (by_mass) mass += ((uint64_t)o->h.hi[i] << 16) + o->h.lo[i];
       }
-      // (a relative weight is at most 2^30 1.022: by mass a lower bound of the count)
-      s0->all.count[i] = by_mass ? (uint32_t)((mass >> 30) - (mass >> 35)) : cnt;
-      s0->all.mass[i] = (mass << (kUnit - 30)) >> (level == 0 ? i / kPerOctave : octave);
+      // (by mass a lower bound of the count: a weight is at most 2^most 1.022 of the bin's units)
+      const int of = level == 0 ? i / kPerOctave : octave, most = max(kUnit - max(of, kUp - 1), 0);
+      s0->all.count[i] = by_mass ? (uint32_t)((mass >> most) - (mass >> (most + 5))) : cnt;
+      s0->all.mass[i] = mass << bin_unit(of);
     }
     if (tid < 2) s.part_n[tid] = 0;
     cluster.sync();
@@ -515,9 +522,6 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
         target = s.cut_target;
       }
       mb += before;
-      int last = -1;  // the thread's last bin that counts
-      uint64_t last_before = 0;
-      uint32_t last_count = 0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const bool here = by_mass ? mb < target && target <= mb + mass[j] : cb < need && need <= cb + cnt[j];
@@ -528,24 +532,8 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
           s.cut_front = cb;
           s.cut_before = mb;
         }
-        if (by_mass ? mass[j] > 0 : cnt[j] > 0) last = tid * kPer + j, last_before = mb, last_count = cnt[j];
         cb += cnt[j];
         mb += mass[j];
-      }
-      __syncthreads();
-      if (s.cut_bin < 0 && !quick) {  // the bins' masses, each rounded down, end a little below the target: the last bin that counts
-        const int best = __reduce_max_sync(0xffffffffu, last);
-        if (lane == 0) s.wcnt[warp] = (uint32_t)(best + 1);
-        __syncthreads();
-        int all = 0;
-        for (int w = 0; w < kSWarps; ++w) all = max(all, (int)s.wcnt[w]);
-        if (last >= 0 && last == all - 1) {
-          s.cut_bin = last;
-          s.cut_count = last_count;
-          s.cut_need = last_count;
-          s.cut_front = kList + 1;
-          s.cut_before = last_before;
-        }
       }
     }
     cluster.sync();
@@ -622,11 +610,9 @@ __device__ bool find_cut(cg::cluster_group& cluster, Shared& s, Shared* s0, cons
             draw_from_list(s, v, to, by_mass ? target : 0);
           } else {
             const Ranked r = rank_list(s, v, to);
-            // the need-th; or the one whose weight takes the mass to the target: the
-            // first or the last where rounding has put the target before or behind them
+            // the need-th, or the one whose weight takes the mass to the target
             const uint64_t front = before + r.front;
-            const bool first = r.place == 0, last = r.place == (uint32_t)to - 1;
-            if (r.place < (uint32_t)to && (by_mass ? (first || front < target) && (last || target <= front + r.w) : r.place == need - 1))
+            if (by_mass ? front < target && target <= front + r.w : r.place == need - 1)
               s.cut = Cut{key_in(r.e), idx_in(r.e)};
           }
         }
