@@ -76,10 +76,8 @@ __device__ __forceinline__ Seq seq_at(const KvArgs& a, int b) {
 }
 
 __device__ __forceinline__ void flag_batch(const KvArgs& a, int b) {
-  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), len = __ldg(a.lens + b);
-  int bad = 0;
-  if (c0 < 0 || c1 < c0 || c1 - c0 > a.max_tokens || c1 > a.n_tokens || c1 - c0 > len) bad |= MOE_KV_BAD_BATCH;
-  if (len > a.max_pages * a.page_size) bad |= MOE_KV_BAD_PAGE;
+  int bad = kv_seq_ok(a, b) ? 0 : MOE_KV_BAD_BATCH;
+  if (__ldg(a.lens + b) > a.max_pages * a.page_size) bad |= MOE_KV_BAD_PAGE;
   if (bad) kv_flag(a, bad);
 }
 

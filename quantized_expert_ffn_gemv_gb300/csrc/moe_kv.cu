@@ -165,6 +165,27 @@ __device__ __forceinline__ uint2 quantise8(const uint32_t (&w)[4], uint16_t& sca
   return make_uint2(((even & 0x0F0F0F0Fu) | (odd << 4 & 0xF0F0F0F0u)) ^ 0x88888888u, 0u);
 }
 
+// The first blocks look through the batch's sequences, a thread one or (with few threads) several.  A thread's first is
+// loaded beside what finds its own token, so that looking costs no trip to memory of its own.
+struct SeqCheck {
+  bool on;  // the block has sequences to look at
+  int64_t b;
+  int c0, c1, len;
+  __device__ __forceinline__ SeqCheck(const KvArgs& kv)
+      : on(blockIdx.y == 0 && blockIdx.x < (unsigned)(kv.n_seqs + kRowThreads - 1) / kRowThreads), c0(0), c1(0), len(0) {
+    if (!on) return;
+    b = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+    if (b < kv.n_seqs) c0 = __ldg(kv.cu + b), c1 = __ldg(kv.cu + b + 1), len = __ldg(kv.lens + b);
+  }
+  __device__ __forceinline__ void flag(const KvArgs& kv) const {
+    if (!on) return;
+    bool ok = kv_seq_ok(kv, c0, c1, len);
+    const int64_t threads = (int64_t)gridDim.x * kRowThreads;
+    for (int64_t i = b + threads; i < kv.n_seqs; i += threads) ok &= kv_seq_ok(kv, (int)i);
+    if (!ok) kv_flag(kv, MOE_KV_BAD_BATCH);
+  }
+};
+
 // LPR lanes a row.  NORM: q and k rows are normalised and rotated.  BITS > 0:
 // k and v rows go to the cache (else k goes to ko and there is no v).
 // blockIdx.y is a unit's place within its token, so that all of a block's
@@ -196,18 +217,19 @@ __global__ void __launch_bounds__(kRowThreads, 4) head_rows_kernel(const RowArgs
 
   int pos = 0;
   uint8_t* tile = nullptr;
-  if (STORE && live) {
-    const int b = kv_seq_of(kv, t);
-    live = b >= 0;
+  if constexpr (STORE) {
+    const SeqCheck seqs(kv);
     if (live) {
-      const int c0 = __ldg(kv.cu + b), fresh = __ldg(kv.cu + b + 1) - c0, len = __ldg(kv.lens + b);
-      pos = len - fresh + (t - c0);
-      if (pos >= 0) tile = kv_tile_of(kv, b, pos, kv_tile_bytes(LPR * 8, BITS));
-      if (flags) {
-        const int bad = (fresh > len || fresh > kv.max_tokens ? MOE_KV_BAD_BATCH : 0) | (pos >= 0 && !tile ? MOE_KV_BAD_PAGE : 0);
-        if (bad) kv_flag(kv, bad);
+      const int b = kv_seq_of(kv, t);
+      live = b >= 0;
+      if (live) {
+        const int c0 = __ldg(kv.cu + b), fresh = __ldg(kv.cu + b + 1) - c0, len = __ldg(kv.lens + b);
+        pos = len - fresh + (t - c0);
+        if (pos >= 0) tile = kv_tile_of(kv, b, pos, kv_tile_bytes(LPR * 8, BITS));
+        if (flags && pos >= 0 && !tile) kv_flag(kv, MOE_KV_BAD_PAGE);
       }
     }
+    seqs.flag(kv);
   }
   const int row = pos & (kKvTile - 1);
   const bool turns = NORM && kind < 2;
@@ -320,16 +342,14 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const KvArgs kv, c
   constexpr int D = LPR * 8, R = kv_row_bytes(D, BITS), HB = kv_half_bytes(D, BITS);
   const int lane = threadIdx.x % LPR;
   const int s = blockIdx.y, t = (int)(blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR);
-  if (t >= kv.n_tokens) return;
-  const int b = kv_seq_of(kv, t);
+  const SeqCheck seqs(kv);
+  const int b = t < kv.n_tokens ? kv_seq_of(kv, t) : -1;
+  seqs.flag(kv);
   if (b < 0) return;
   const int c0 = __ldg(kv.cu + b), n = __ldg(kv.cu + b + 1) - c0, len = __ldg(kv.lens + b);
   const int pos = len - n + (t - c0);
   const uint8_t* tile = pos >= 0 ? kv_tile_of(kv, b, pos, kv_tile_bytes(D, BITS)) : nullptr;
-  if (lane == 0 && s == 0) {
-    const int bad = (n > len || n > kv.max_tokens ? MOE_KV_BAD_BATCH : 0) | (pos >= 0 && !tile ? MOE_KV_BAD_PAGE : 0);
-    if (bad) kv_flag(kv, bad);
-  }
+  if (lane == 0 && s == 0 && pos >= 0 && !tile) kv_flag(kv, MOE_KV_BAD_PAGE);
   const int row = pos & (kKvTile - 1), turn = kv_turn(row) & (R / 16 - 1);
   const int at = BITS == 8 ? row * R + (((lane >> 1) ^ turn) << 4) + (lane & 1) * 8
                            : row * R + (((lane >> 2) ^ turn) << 4) + (lane & 3) * 4;

@@ -65,6 +65,14 @@ __device__ __forceinline__ int kv_seq_of(const KvArgs& a, int t) {
   return -1;
 }
 
+// Whether a sequence's new tokens c0 .. c1 - 1 can be: an ascending share of the rows, no more of them than the call or the sequence has.
+__device__ __forceinline__ bool kv_seq_ok(const KvArgs& a, int c0, int c1, int len) {
+  return c0 >= 0 && c1 >= c0 && c1 <= a.n_tokens && c1 - c0 <= min(a.max_tokens, len);
+}
+__device__ __forceinline__ bool kv_seq_ok(const KvArgs& a, int b) {
+  return kv_seq_ok(a, __ldg(a.cu + b), __ldg(a.cu + b + 1), __ldg(a.lens + b));
+}
+
 // The 32-token tile that holds position pos (>= 0) of sequence b, head 0, or
 // NULL for a bad page.
 __device__ __forceinline__ uint8_t* kv_tile_of(const KvArgs& a, int b, int pos, int tile_bytes) {
