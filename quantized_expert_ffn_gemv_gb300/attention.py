@@ -80,6 +80,13 @@ def _on_gpu(t, name):
     return dev
 
 
+def _int32(**sizes):
+    """The library's sizes are 32-bit, and ctypes would pass on the low bits of a larger one."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name}: {v} is beyond 32 bits")
+
+
 def _rows(t, name, shape, dtype, dev, out=False):
     """Address and strides of a [tokens, heads, D] tensor, checked."""
     if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
@@ -109,6 +116,7 @@ def rope_table(n_positions, rot_dim, base, device="cuda"):
     float32 [n_positions, rot_dim / 2, 2] on `device`."""
     if n_positions < 1 or rot_dim < 16 or rot_dim % 16:
         raise ValueError("n_positions must be positive and rot_dim a positive multiple of 16")
+    _int32(n_positions=n_positions, rot_dim=rot_dim)
     t = np.empty((n_positions, rot_dim // 2, 2), np.float32)
     moe.check(moe.lib().moe_rope_table(n_positions, rot_dim, base, t.ctypes.data), "moe_rope_table")
     return torch.from_numpy(t).to(device)
@@ -124,6 +132,7 @@ def _norm_rope(dtype, dim, dev, table, q_weight, k_weight, eps, interleaved, wei
         if table.get_device() != dev:
             raise ValueError(f"table must be a CUDA tensor on cuda:{dev}, got {table.device}")
         n_positions, rot, at = shape[0], 2 * shape[1], table.data_ptr()
+        _int32(n_positions=n_positions, rot_dim=rot)
     return moe.NormRope(_vector(q_weight, "q_weight", dtype, dim, dev), _vector(k_weight, "k_weight", dtype, dim, dev), at,
                         n_positions, rot, 1 if interleaved else 0, eps, weight_offset)
 
@@ -144,6 +153,7 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6,
         raise ValueError("q and k must be [T, heads, D]")
     T, nq, dim = q_shape = q.shape
     nk = k.shape[1]
+    _int32(tokens=T, q_heads=nq, k_heads=nk, head_dim=dim)
     k_shape = (T, nk, dim)
     dtype = q.dtype
     code = _code(dtype, "q")
@@ -189,6 +199,7 @@ class KvBatch:
         max_tokens = n_tokens if max_tokens is None else int(max_tokens)
         if n_tokens < 0 or (n_tokens and not 1 <= max_tokens <= n_tokens):
             raise ValueError("max_tokens must lie in 1..n_tokens")
+        _int32(n_tokens=n_tokens, n_seqs=n_seqs, max_pages=max_pages, table_stride=stride)
         self._tensors = (block_table, seq_lens, cu_tokens)
         self.dev, self.n_seqs, self.n_tokens, self.max_tokens = dev, n_seqs, n_tokens, max_tokens
         self.desc = moe.KvBatchDesc(block_table.data_ptr(), _vector(seq_lens, "seq_lens", _i32, n_seqs, dev),
@@ -205,6 +216,7 @@ class KvCache:
     or None to allocate one."""
 
     def __init__(self, n_pages, page_size, n_kv_heads, head_dim, bits=8, device=0, data=None):
+        _int32(n_pages=n_pages, page_size=page_size, n_kv_heads=n_kv_heads, head_dim=head_dim, bits=bits)
         page = int(moe.lib().moe_kv_page_bytes(page_size, n_kv_heads, head_dim, bits))
         if not page or n_pages < 1:
             raise ValueError("page_size a multiple of 32 up to 4096, head_dim 64, 128 or 256, bits 8 or 4, n_pages >= 1")
@@ -260,6 +272,7 @@ class KvCache:
         dtype, T, dim, dev = q.dtype, batch.n_tokens, self.head_dim, self.dev
         code = _code(dtype, "q")
         nq = q.shape[1]
+        _int32(q_heads=nq)
         q_shape, kv = (T, nq, dim), (T, self.n_kv_heads, dim)
         qr, kr, vr = _rows(q, "q", q_shape, dtype, dev), _rows(k, "k", kv, dtype, dev), _rows(v, "v", kv, dtype, dev)
         scope = self._enter(batch, stream)
@@ -321,6 +334,7 @@ class KvCache:
             raise ValueError("q must be [n_tokens, heads, head_dim]")
         dtype, T, nq, dim, dev = q.dtype, batch.n_tokens, q.shape[1], self.head_dim, self.dev
         shape = (T, nq, dim)
+        _int32(q_heads=nq, shared_tokens=shared_tokens)
         code = _code(dtype, "q")
         qr = _rows(q, "q", shape, dtype, dev)
         lse_at = None

@@ -3,7 +3,7 @@ include/moe_model.h).  Argument marshalling only."""
 import torch
 
 from . import moe
-from .attention import _f32, _i32, _native, _on_gpu, _raw_stream, _scope, _vector
+from .attention import _f32, _i32, _int32, _native, _on_gpu, _raw_stream, _scope, _vector
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -25,6 +25,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     if code is None:
         raise ValueError(f"logits: expected bfloat16, float16 or float32, got {logits.dtype}")
     rows, vocab = logits.shape
+    _int32(rows=rows, vocab=vocab)
     stride, es = logits.stride()
     if rows <= 1:
         stride = vocab
