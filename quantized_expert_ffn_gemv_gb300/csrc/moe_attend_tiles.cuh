@@ -223,7 +223,7 @@ struct Walk {
       const int last = min((lo + 1) * ROWS, s.n * t.group) - 1;
       p.lim = min(s.len, a.max_pages * a.page_size);
       const int lim = t.shared ? p.lim : min(s.len - s.n + last / t.group + 1, p.lim);
-      p.steps = max(1, (lim + kKeys - 1) / kKeys);
+      p.steps = lim > 0 ? (lim - 1) / kKeys + 1 : 1;
       auto step_at = [&](long long pos) {
         const long long u = quotient<ROWS>(pos, t.group) - kSegmentKeys;
         return (int)min((long long)p.steps, (max(u, 0ll) + kKeys - 1) / kKeys);

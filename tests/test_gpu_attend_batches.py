@@ -177,3 +177,26 @@ def test_prefix_pass_of_either_type_and_page(bits, dim, dtype, page, share, seqs
     out = cache.attend(q, batch, lse=lse, shared_tokens=share)
     cache.check()
     check(f64(q), f64(out), f64(lse), kv, news, lens, dim ** -0.5, q.dtype, keys_rounded=True)
+
+
+@pytest.mark.parametrize("n", [1, 9])
+def test_the_longest_sequence(n):
+    """2^31 - 32 positions, all on one page of 32: a softmax over that page's tokens, the sum 2^26 - 1 times as large.  The sums
+    of equal terms in fp32 are off by up to half a unit of the running sum a term: of 2^30 where a term is 2^14, 2^-8 of it; and
+    the tensor core's accumulator by twice that, as it truncates."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import attention
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    pages, group, dim = 2 ** 26 - 1, 8, 64
+    cache = attention.KvCache(1, 32, 1, dim, 4)
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    kv = fill(cache, np.zeros((1, 1), np.int32), [32])
+    batch = attention.KvBatch(table, i32(32 * pages), i32(0, n), n, n)
+    q = torch.randn(n, group, dim, device="cuda").bfloat16()
+    lse = torch.zeros(n, group, device="cuda")
+    out = cache.attend(q, batch, lse=lse)
+    cache.check()
+    for i in range(n):  # (that the first of them see eight keys less is 2^-28 of the sum)
+        want, want_l = ref.attend(f64(q[i:i + 1]), *kv[0], dim ** -0.5, 1)
+        assert np.abs(f64(lse[i:i + 1]) - want_l - np.log(pages)).max() <= 2.0 ** -6
+        assert np.abs(f64(out[i:i + 1]) - want).max() <= (2.0 ** -6 + 2.0 ** -8) * np.abs(kv[0][1]).max()
