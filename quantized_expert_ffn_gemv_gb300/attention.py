@@ -87,6 +87,16 @@ def _int32(**sizes):
             raise ValueError(f"{name}: {v} is beyond 32 bits")
 
 
+def _apart(n_tokens, n_heads, dim, ts, hs):
+    """No two of the rows share an element (as the library checks it)."""
+    if n_tokens < 2 or n_heads < 2:
+        return (n_tokens < 2 or ts >= dim) and (n_heads < 2 or hs >= dim)
+    (far, n_far), (near, n_near) = sorted(((ts, n_tokens), (hs, n_heads)), reverse=True)
+    if near < dim or (n_near - 1) * near + dim <= far:
+        return near >= dim
+    return all(abs(j * near - i * far) >= dim for j in range(1, n_near) for i in (j * near // far, j * near // far + 1) if 0 < i < n_far)
+
+
 def _rows(t, name, shape, dtype, dev, out=False):
     """Address and strides of a [tokens, heads, D] tensor, checked."""
     if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
@@ -94,7 +104,7 @@ def _rows(t, name, shape, dtype, dev, out=False):
         at = t.data_ptr()
         if es != 1 or (ts | hs) & 7 or at & 15:
             raise ValueError(f"{name}: heads must be contiguous, strides multiples of 8 elements and data 16-byte aligned")
-        if out and ((shape[0] > 1 and ts < shape[2]) or (shape[1] > 1 and hs < shape[2])):
+        if out and not _apart(*shape, ts, hs):
             raise ValueError(f"{name}: rows of an output must not overlap")
         return at, ts, hs
     if t.dtype is not dtype or tuple(t.shape) != tuple(shape):

@@ -103,6 +103,7 @@ static int as_rows(const tensor_t* t, PyObject* dtype, long dev, int64_t n0, int
   if (t->ndim != 3 || t->dtype != dtype || t->dev != dev || t->shape[0] != n0 || t->shape[1] != n1 || t->shape[2] != n2) return 0;
   if (t->stride[2] != 1 || ((t->stride[0] | t->stride[1]) & 7) || (t->at & 15)) return 0;
   if (out && ((n0 > 1 && t->stride[0] < n2) || (n1 > 1 && t->stride[1] < n2))) return 0;
+  if (out && n0 > 1 && n1 > 1 && t->stride[0] < (n1 - 1) * t->stride[1] + n2 && t->stride[1] < (n0 - 1) * t->stride[0] + n2) return 0;
   h->data = (void*)t->at;
   h->token_stride = t->stride[0];
   h->head_stride = t->stride[1];

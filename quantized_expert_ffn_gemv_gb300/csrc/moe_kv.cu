@@ -7,6 +7,7 @@
 // 16-byte load) each, so the mean square is a butterfly over those lanes, a
 // rotation partner is one shuffle away and a scale block of 32 is 4 lanes.
 #include <cmath>
+#include <utility>
 
 #include "moe_kv.cuh"
 
@@ -41,8 +42,27 @@ bool heads_ok(const moe_heads_t* h, int dim) {
          (h->head_stride == 0 || h->head_stride >= dim);
 }
 
+// No two of n_tokens x n_heads rows of dim elements share one.
+static bool rows_apart(int64_t n_tokens, int64_t n_heads, int64_t ts, int64_t hs, int64_t dim) {
+  if (n_tokens < 2 && n_heads < 2) return true;
+  if (n_heads < 2) return ts >= dim;
+  if (n_tokens < 2) return hs >= dim;
+  if (ts < hs) std::swap(ts, hs), std::swap(n_tokens, n_heads);
+  using wide = __int128;
+  if (hs < dim) return false;
+  if ((wide)(n_heads - 1) * hs + dim <= ts) return true;  // the usual ones
+  // the smaller steps end up among later rows of the larger: the distance of each to the two nearest of those
+  for (int64_t j = 1; j < n_heads; ++j) {
+    const wide at = (wide)j * hs;
+    const int64_t i = (int64_t)(at / ts);
+    if ((i > 0 && i < n_tokens && at - (wide)i * ts < dim) || (i + 1 < n_tokens && (wide)(i + 1) * ts - at < dim)) return false;
+    if (i >= n_tokens) break;  // behind all of them
+  }
+  return true;
+}
+
 bool out_heads_ok(const moe_heads_t* h, int n_heads, int n_tokens, int dim) {
-  return heads_ok(h, dim) && (n_heads <= 1 || h->head_stride) && (n_tokens <= 1 || h->token_stride);
+  return heads_ok(h, dim) && rows_apart(n_tokens, n_heads, h->token_stride, h->head_stride, dim);
 }
 
 moe_status_t device_sms(int* sms) {
@@ -498,6 +518,7 @@ extern "C" MOE_API moe_status_t moe_qk_norm_rope(const moe_norm_rope_t* desc, in
   st = moe::norm_args(desc, head_dim, positions, n_tokens > 0, &r);
   if (st != MOE_OK) return st;
   if (n_tokens == 0 || n_q + n_kv == 0) return MOE_OK;
+  if (n_q + n_kv > 65535) return MOE_ERR_UNSUPPORTED;
   if (n_q && (!moe::heads_ok(q, head_dim) || !moe::out_heads_ok(q_out, n_q, n_tokens, head_dim))) return MOE_ERR_INVALID_ARG;
   if (n_kv && (!moe::heads_ok(k, head_dim) || !moe::out_heads_ok(k_out, n_kv, n_tokens, head_dim))) return MOE_ERR_INVALID_ARG;
   r.q = moe::src_of(n_q ? q : nullptr);
