@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
       if (sent >= 2 * nt) return;
       const int i = sent >> 1;
       if (i >= first + 32) load_pages(i);
-      if (lane == i - first) {
+      if (lane == i - first && in_time) {  // (an entry whose copy did not come is not filled again)
         mbar_expect_tx(bars + in_slot * 8, P::kHalf);
         bulk_g2s(ring + in_slot * P::kHalf, mine_src + (sent & 1) * P::kHalf, P::kHalf, bars + in_slot * 8);
       }
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
         if (g == 0) s_stat[warp][8 * n + 2 * tq + h] = make_float2(m[n][h], l[n][h]);
       }
 
-    // merge: the ring is drained (every half issued was used)
+    // merge: the ring is drained (every half issued was used, unless a wait ran out)
     float* mine_o = merge + warp * (P::kRing / 4);
     __syncwarp();
     if (nt > 0) {
@@ -578,6 +578,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
       }
     }
   }
+  if (!in_time) settle();
   if (t.shared) grid_wait();  // the merge waits for this kernel, and through it for the prefix's pass
 }
 

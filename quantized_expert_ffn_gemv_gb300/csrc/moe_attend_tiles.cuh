@@ -473,9 +473,9 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
           for (int v = 0; v < 2; ++v) {
             const int e = v * P::kEntries + entry;
             mbar_wait(bar(kRawEmpty + e), phase, ok);
-            if (lane == 0) mbar_expect_tx(bar(kRawFull + e), P::kEntry);
+            if (lane == 0 && ok) mbar_expect_tx(bar(kRawFull + e), P::kEntry);  // (who has not seen the entry given back does not fill it)
             __syncwarp();
-            if (lane >= (i & 31) && lane < (i & 31) + P::kHalves)
+            if (ok && lane >= (i & 31) && lane < (i & 31) + P::kHalves)
               bulk_g2s(sm + P::kOffRaw + e * P::kEntry + (lane - (i & 31)) * P::kHalf, src + v * P::kHalf, P::kHalf, bar(kRawFull + e));
           }
           if (++entry == P::kEntries) entry = 0, phase ^= 1;
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
     }
   }
   tc_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) settle();
   tc_after();
   if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(P::kTmemCols));

@@ -45,6 +45,12 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool& ok) {
   if (!mbar_try_wait(bar, parity) && ok) ok = mbar_wait_slow(bar, parity);
 }
+// Where a wait ran out: a tenth of a second for the copies and products still in flight, so that none ends in shared or
+// tensor memory that the block has given back.  (They take microseconds; what issues them has stopped.)
+__device__ __forceinline__ void settle() {
+  const uint64_t start = now_ns();
+  for (int i = 0; i < 100000 && now_ns() - start < 100000000ull; ++i) __nanosleep(1000);
+}
 __device__ __forceinline__ void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
 // Orders this thread's ordinary shared-memory accesses before later
 // asynchronous ones (bulk copies, tcgen05 operands).
