@@ -417,9 +417,10 @@ HeadDst dst_of(const moe_heads_t* h) {
 template <int LPR, bool NORM, int BITS>
 moe_status_t launch_rows(RowArgs r, const KvArgs& kv, bool bf16, cudaStream_t st) {
   const int64_t H = (int64_t)r.nq + r.nk + (BITS ? r.nk : 0);
-  // One row a group while that fills the GPU at most once over, so that a
-  // small call's rows all run side by side; several rows of a token a group
-  // above that, which reuses the token's angles and page.
+  // One row a group while its threads fill the 152 SMs (1,024 of them each, by
+  // the launch bounds) at most twice over, so that a small call's rows run
+  // side by side; several rows of a token a group above that, which reuses the
+  // token's angles and page.
   if (H > 65535) return MOE_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)r.n_tokens * H;
   r.per = rows * LPR <= 152 * 2048 ? 1 : kRowsPerUnit;

@@ -915,7 +915,7 @@ moe_status_t launch_sample(SampleArgs a, cudaStream_t st) {
   int sms = 0;
   moe_status_t ok = device_sms(&sms);
   if (ok != MOE_OK) return ok;
-  // Slices of at most 80 KB leave room for two CTAs an SM; few rows take larger
+  // Slices of at most 80 KB leave room for two CTAs an SM (larger rows than 163,840 words go without); few rows take larger
   // clusters, down to slices of 4,096, so that one row's read and passes are
   // spread over more SMs.
   int C = 1;
@@ -925,7 +925,8 @@ moe_status_t launch_sample(SampleArgs a, cudaStream_t st) {
   const int smem = (int)sizeof(Shared) + a.slice * 4;
   ok = raise_smem<sample_kernel<T>>((int)sizeof(Shared) + kMaxVocab / kMaxCluster * 4);
   if (ok != MOE_OK) return ok;
-  a.ahead = std::max(1, sms * (smem <= 110 * 1024 ? 2 : 1) / C);
+  // what runs at a time: an SM's 228 KB hold two CTAs (with 1 KB each of the system's) up to slices of 20,480
+  a.ahead = std::max(1, sms * (2 * (smem + 1024) <= 228 * 1024 ? 2 : 1) / C);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.rows * C));
   cfg.blockDim = dim3(kSThreads);
