@@ -10,7 +10,7 @@
  * device, allocate nothing and can be captured in a CUDA graph.  A call keeps
  * no state: two calls may run at once on different streams when neither
  * writes what the other reads or writes (a workspace included).
- * On an error nothing is launched.
+ * On an error nothing is launched.  All are forward operators.
  */
 #ifndef MOE_MODEL_GB300_H
 #define MOE_MODEL_GB300_H
@@ -28,7 +28,8 @@ enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 };
  * Rows of heads, [token][head][D]: the elements of a head are contiguous;
  * strides count elements and are multiples of 8, data is 16-byte aligned.
  * A slice of a packed projection (q, k and v of a token side by side) is one.
- * Inputs may repeat rows (a stride of 0); rows of an output are distinct.
+ * Inputs may repeat rows (a stride of 0); rows of an output may not overlap
+ * (INVALID_ARG).
  */
 typedef struct {
   void* data; /* device */
@@ -102,8 +103,8 @@ MOE_API moe_status_t moe_qk_norm_rope(const moe_norm_rope_t* desc, int32_t dtype
  */
 enum {
   MOE_KV_BAD_PAGE = 1,   /* a block-table entry outside 0..n_pages-1, or a length beyond the table's width, was met */
-  MOE_KV_BAD_BATCH = 2,  /* cu_tokens not ascending, or a sequence with more new tokens than its length or than max_tokens */
-  MOE_KV_TIMEOUT = 4     /* a wait inside a kernel ran out: outputs are invalid */
+  MOE_KV_BAD_BATCH = 2,  /* cu_tokens not ascending or beyond n_tokens, or a sequence with more new tokens than its length or than max_tokens */
+  MOE_KV_TIMEOUT = 4     /* a wait inside a kernel (two seconds) ran out: outputs are invalid */
 };
 
 typedef struct {
@@ -135,7 +136,8 @@ typedef struct {
   int32_t table_stride;       /* entries from one row of block_table to the next, >= max_pages */
   int32_t max_pages;          /* entries of a row, >= 1; max_pages * page_size < 2^31 */
   int32_t n_tokens;           /* rows of q, k, v and the outputs, >= cu_tokens[n_seqs], < 2^31 - 256; 0: the call does nothing */
-  int32_t max_tokens;         /* the most new tokens of one sequence, 1..n_tokens */
+  int32_t max_tokens;         /* the most new tokens of one sequence, 1..n_tokens; the attention is planned for it: a loose bound
+                                 is right, but takes a decode batch to the kernel for prompts, at about twice the time */
 } moe_kv_batch_t;
 
 /* Bytes of one page, 0 when the arguments are not a cache's. */
@@ -182,8 +184,11 @@ MOE_API moe_status_t moe_kv_read(const moe_kv_cache_t* cache, const moe_kv_batch
  * and otherwise only the probabilities: what the other roundings leave is a
  * second operand.  lse (fp32 [n_tokens][n_q], or NULL): the natural
  * logarithm of the sum of exp(score).  A token of negative position sees
- * nothing: its out is 0 and its lse -infinity.  A row that meets a bad page
- * is NaN.  What lies in pages behind the position a row sees never reaches that row.
+ * nothing: its out is 0 and its lse -infinity.  A row that sees a bad page, or
+ * a position behind the table's width, is NaN.  One that sees a value block of
+ * NaN is NaN in the block's elements at least, and may be in all, its lse
+ * included.  What lies behind the position a row sees never reaches that row.
+ * out may be q; other overlaps are not allowed.
  * shared_tokens (a multiple of page_size, 0 = off) says that the block tables
  * of all sequences begin with the same pages up to that position, so that
  * those keys may be read once for the whole batch, which is done where it

@@ -5,7 +5,8 @@ Argument marshalling only.  Shapes, dtypes, strides and devices are checked
 here, so a mismatched tensor is a ValueError and never an out-of-bounds device
 access; the contents of the batch's index arrays are checked on the device
 (``KvCache.check``).  Calls run on ``stream``, or on the current stream of the
-tensors' device; tensors they return are allocated there.
+tensors' device; tensors they return are allocated there.  The operators are
+forward ones: what they return carries no gradient.
 
 A decode step makes several of these calls a layer, so each function first
 offers its arguments to the extension module (csrc/binding.c), which makes
@@ -194,8 +195,9 @@ class KvBatch:
     seq_lens int32 [n_seqs] (positions that hold tokens, new ones included),
     cu_tokens int32 [n_seqs + 1] (rows of the new tokens, from 0), n_tokens
     rows in all (a padded batch may have more than cu_tokens[-1]), at most
-    max_tokens of one sequence.  The arrays stay where they are and are read
-    when a call runs."""
+    max_tokens of one sequence (None: n_tokens, which is right for any batch,
+    but plans the attention for one long prompt: pass 1 for decode).  The
+    arrays stay where they are and are read when a call runs."""
 
     def __init__(self, block_table, seq_lens, cu_tokens, n_tokens, max_tokens=None):
         if block_table.dim() != 2 or block_table.dtype is not _i32 or block_table.stride(1) != 1:
@@ -335,7 +337,7 @@ class KvCache:
         n_q] to receive the log-sum-exp, or None.  shared_tokens: leading
         positions (a multiple of page_size) whose pages are the same in every
         row of the block table; they are then read once for the whole batch.
-        Returns out.  See moe_kv_attend."""
+        out may be q.  Returns out.  See moe_kv_attend."""
         if stream is None and batch.dev == self.dev:
             r = (_native_module or _native()).attend(self._at, batch._at, self.dev, self.data, q, scale, out, lse, shared_tokens)
             if r is not None:

@@ -264,7 +264,7 @@ moe_status_t attend_plan(const moe_kv_cache_t* cache, const moe_kv_batch_t* batc
   // and 107, 121 and 185, 124 and 190); heads of 64, 64 rows: 109 and 117 (4 bits
   // 101 and 112; with fp16 activations the tiles take a third longer, rows do
   // not).  Heads of 256, which have registers for 16 rows here: 12
-  // sequences of 60,000 to 131,072 tokens in 4 bits, 32 rows, 226 and 328.
+  // sequences of 60,000 to 131,072 tokens in 4 bits, 32 rows, 219 and 328.
   const int dim = cache->head_dim, heads = cache->n_kv_heads, group = n_q / heads;
   const int big = dim == 256 ? 128 : 256;
   p->tiles = rows > (dim == 256 ? 16 : dim == 128 ? 32 : 64);

@@ -26,8 +26,8 @@
 // while the other's softmax runs.  A step of 64 keys (heads of 128, 256 rows)
 // is 24 products, 1,240 cycles of the tensor core; one warp that issued both
 // tiles' products, with its waits and elections, took 2,500.  2,048 new tokens
-// of 4,096 (32 query and 4 kv heads of 128, 8 bits, bf16) take 230 us, 8,192 of
-// 16,384 1,350 (1,220 TFLOP/s); the chain of a step's softmax bounds them.
+// of 8,192 (32 query and 4 kv heads of 128, 8 bits, bf16) take 230 us (1,046
+// TFLOP/s), 8,192 of 16,384 1,350 (1,220); the chain of a step's softmax bounds them.
 //
 // The line of work is measured in keys, causal limits included, so that all
 // parts cost the same: row tile rt of a sequence costs kSegmentKeys + the keys
@@ -172,9 +172,11 @@ struct Piece {
 };
 
 // a / b of numbers >= 0, mostly of 31 bits, when a shorter division does: 2,048
-// new tokens of 4,096 take 230 us with it and 242 without.  Not with row tiles
-// of 128 (heads of 256), where the rest of the kernel comes out slower for it:
-// 12 long sequences in 4 bits 226 us without and 245 with it.
+// new tokens of 8,192 take 230 us with it and 242 without.  Not with row tiles
+// of 128 (heads of 256), where the kernel comes out slower for it in every case
+// measured, of unknown cause: 12 sequences of 60,000 to 131,072 tokens in 4
+// bits 219 us without and 250 with it, 16 of 16,384 with 24 rows each 71 and 83, in
+// 8 bits 81 and 89.
 template <int ROWS>
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ROWS == 256 && ((a | b) >> 31) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;

@@ -13,8 +13,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     be strided) from uniform numbers u float32 [rows] in [0, 1).  temperature
     float32, top_k int32, top_p float32 and min_p float32 hold one value a row;
     None leaves the step out (temperature 1).  Returns (tokens int32 [rows],
-    probs float32 [rows]: the token's share of the kept mass); a row without a
-    logit above -infinity gives token -1."""
+    probs float32 [rows]: the token's share of the kept mass, without a
+    gradient); a row without a logit above -infinity gives token -1."""
     if stream is None:
         r = _native().sample(logits, u, temperature, top_k, top_p, min_p, tokens, probs)
         if r is not None:

@@ -200,3 +200,48 @@ def test_the_longest_sequence(n):
         want, want_l = ref.attend(f64(q[i:i + 1]), *kv[0], dim ** -0.5, 1)
         assert np.abs(f64(lse[i:i + 1]) - want_l - np.log(pages)).max() <= 2.0 ** -6
         assert np.abs(f64(out[i:i + 1]) - want).max() <= (2.0 ** -6 + 2.0 ** -8) * np.abs(kv[0][1]).max()
+
+
+@pytest.mark.parametrize("news,lens", [([1] * 5, [1, 40, 700, 33, 9000]), ([2, 1, 7], [5, 300, 64]), ([300, 2, 90], [300, 1000, 2500])])
+def test_out_may_be_q(news, lens):
+    """In place, on both kernels, with segments that one CTA finishes and such as are joined: the bits of the other call."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import attention
+    rng = np.random.default_rng(len(lens))
+    batch, table, n_pages = make_batch(news, lens, 64, rng, pad_rows=2)
+    cache = attention.KvCache(n_pages, 64, 2, 128, 8)
+    fill(cache, table, lens)
+    q = torch.randn(batch.n_tokens, 8, 128, device="cuda").bfloat16()
+    want, x = q.clone(), q.clone()  # (rows behind the last sequence stay q's)
+    cache.attend(q, batch, out=want)
+    assert cache.attend(x, batch, out=x) is x
+    cache.check()
+    assert torch.equal(x, want)
+
+
+def test_out_may_be_q_behind_a_prefix():
+    import torch
+    cache, batch, _, q, _, _, _ = prefix_case(8, 128, "bf16", 64, 1024, 300, 2)
+    want = cache.attend(q, batch, shared_tokens=1024)
+    assert torch.equal(cache.attend(q, batch, out=q, shared_tokens=1024), want)
+    cache.check()
+
+
+@pytest.mark.parametrize("shared", [0, 64])
+def test_no_tokens(shared):
+    """A call without rows does nothing and gives empty results, whatever the sequences hold."""
+    import torch
+    from quantized_expert_ffn_gemv_gb300 import attention
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    cache = attention.KvCache(4, 64, 2, 128)
+    cache.data.fill_(3)
+    batch = attention.KvBatch(i32([0, 1], [2, 3]), i32(100, 0), i32(0, 0, 0), 0)
+    x = torch.empty(0, 2, 128, device="cuda").bfloat16()
+    q = torch.empty(0, 8, 128, device="cuda").bfloat16()
+    cache.append(x, x, batch)
+    assert cache.append_norm_rope(q, x, x, batch, None).shape == q.shape
+    assert [t.shape for t in cache.read(batch)] == [x.shape] * 2
+    assert cache.attend(q, batch, shared_tokens=shared, lse=torch.empty(0, 8, device="cuda")).shape == q.shape
+    assert [t.shape for t in attention.qk_norm_rope(q, x, i32(), None)] == [q.shape, x.shape]
+    cache.check()
+    assert (cache.data == 3).all()
