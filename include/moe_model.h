@@ -124,7 +124,7 @@ typedef struct {
  * seq_lens[b] positions: row cu_tokens[b] + i has position seq_lens[b] -
  * (cu_tokens[b+1] - cu_tokens[b]) + i.  Position p lives in page
  * block_table[b][p / page_size], row p % page_size.  Rows behind
- * cu_tokens[n_seqs] (a padded batch) are neither read nor written.
+ * cu_tokens[n_seqs] (a padded batch) have no effect and are not written.
  * The arrays are read on the device when the call runs, so a captured graph
  * follows their contents.
  */
