@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(kAttThreads, (RowsPlan<D, BITS, NT>::kBlocks))
     bad = __reduce_min_sync(0xffffffffu, bad);
     if (bad != INT32_MAX && lane == 0) kv_flag(a, MOE_KV_BAD_PAGE);
     if (sq.over) bad = min(bad, a.max_pages * a.page_size);  // (flagged with the batch)
+    in_time = __all_sync(0xffffffffu, in_time);
     if (!in_time) {
       if (lane == 0) kv_flag(a, MOE_KV_TIMEOUT);
       bad = INT32_MIN;

@@ -719,10 +719,7 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
       __syncwarp();
       finished();
       if (bad <= see || (p.sq.over && see >= a.max_pages * a.page_size)) l = __uint_as_float(kNaN);
-      if (!ok) {
-        if (lane == 0) kv_flag(a, MOE_KV_TIMEOUT);
-        l = __uint_as_float(kNaN);
-      }
+      if (!ok) l = __uint_as_float(kNaN);
       const bool whole = p.t0 == 0 && p.t1 == p.steps, finish = whole && !t.shared;
       const int64_t segment = (int64_t)p.head * W::row_tiles(t, p.sq) + p.rt;  // (with a shared prefix)
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -768,7 +765,10 @@ __global__ void __launch_bounds__((TilesPlan<D, BITS, BF16>::kThreads), 1) atten
     }
   }
   tc_before();
-  if (__syncthreads_or(!ok)) settle();
+  if (__syncthreads_or(!ok)) {  // (the first wait to run out may be any role's: what it then gives on is taken for good by the others)
+    if (tid == 0) kv_flag(a, MOE_KV_TIMEOUT);
+    settle();
+  }
   tc_after();
   if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(P::kTmemCols));
